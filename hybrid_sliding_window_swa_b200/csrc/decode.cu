@@ -55,7 +55,8 @@ struct WsLayout {
   size_t part_off, part_bytes_per_item, bytes;
   __host__ __device__ WsLayout(int n_seqs, int rows, int d, int64_t max_items) {
     part_off = align256(sizeof(WsHeader) + sizeof(int) * (5 * (size_t)n_seqs + 1));
-    part_bytes_per_item = (size_t)rows * (d + 2) * sizeof(float);
+    // whole 16-byte units: the partials are written and read as float4
+    part_bytes_per_item = ((size_t)rows * (d + 2) * sizeof(float) + 15) & ~(size_t)15;
     bytes = part_off + part_bytes_per_item * (size_t)max_items;
   }
 };
