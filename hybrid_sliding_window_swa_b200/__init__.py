@@ -27,6 +27,7 @@ HSWA_ERR_DEVICE_BOUNDS = -6
 
 HSWA_KV_BF16 = 0
 HSWA_KV_FP8_E4M3 = 1
+HSWA_KV_INT4 = 2
 
 EXPORTED = [
     "kv_pool_layout", "kv_pool_create", "kv_pool_destroy", "kv_pool_append",
@@ -35,7 +36,7 @@ EXPORTED = [
     "hswa_selftest_wait_timeout", "hswa_tree_create", "hswa_tree_destroy", "hswa_tree_insert",
     "hswa_tree_release", "hswa_tree_evict_swa", "hswa_tree_match", "hswa_tree_match_batch", "hswa_tree_stats",
     "hswa_tree_match_slots", "kv_pool_gather_ring", "kv_pool_set_scales", "hswa_shard_kv_heads",
-    "hswa_shard_sequences",
+    "hswa_shard_sequences", "rope_fwd", "kv_pool_append_rope", "hybrid_decode_mod_fwd",
 ]
 
 # scratch bytes available to hybrid_decode_fwd_noalloc (HSWA_NOALLOC_SCRATCH_BYTES in hswa.h)
@@ -54,6 +55,16 @@ class PoolDescC(ctypes.Structure):
         ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
         ("max_seqs", ctypes.c_int32), ("kv_format", ctypes.c_int32), ("pages_per_full_layer", ctypes.c_int64),
     ]
+
+
+class RopeDescC(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("n_axes", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("inv_freq", ctypes.c_double * 64), ("axis", ctypes.c_uint8 * 64)]
+
+
+class ScoreModC(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("dist_slope", ctypes.c_void_p), ("key_begin", ctypes.c_void_p),
+                ("key_end", ctypes.c_void_p)]
 
 
 _lib = None
@@ -93,6 +104,10 @@ def load_library(path: str | None = None):
         "hswa_shard_kv_heads": [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(ctypes.c_int32),
                                 ctypes.POINTER(ctypes.c_int32)],
         "hswa_shard_sequences": [p, ctypes.c_int32, ctypes.c_int32, p, p],
+        "rope_fwd": [ctypes.POINTER(RopeDescC), i32, i64, p, p, p, i32, p, p, i32, p],
+        "kv_pool_append_rope": [p, i32, ctypes.POINTER(RopeDescC), p, i32, p, p, i32, p, p, i32, p, p, p, p, i32, p],
+        "hybrid_decode_mod_fwd": [p, i32, p, p, p, p, i32, i32, p, i64, p, p, i32, i32, ctypes.POINTER(ScoreModC), p,
+                                  sz, p],
         "hswa_tree_evict_swa": [p, p, i64, i64, i64, ctypes.POINTER(i64)],
         "hswa_tree_match": [p, p, i64, ctypes.POINTER(i64), ctypes.POINTER(i64)],
         "hswa_tree_match_batch": [p, p, p, ctypes.c_int32, p, p],
@@ -151,6 +166,10 @@ class PoolDesc:
     def fp8(self) -> bool:
         return self.kv_format == HSWA_KV_FP8_E4M3
 
+    @property
+    def int4(self) -> bool:
+        return self.kv_format == HSWA_KV_INT4
+
 
 def kv_pool_layout(desc: PoolDesc) -> tuple[int, int, int]:
     """(bytes_total, bytes_swa, bytes_full) of the dual pool."""
@@ -172,10 +191,16 @@ class KVPool:
     def _views(self):
         d = self.desc
         _, swa, _full = kv_pool_layout(d)
+        mem = self.memory
+        if d.int4:
+            blk = [r * (d.head_dim // 2) + (r * 4 + 15) // 16 * 16 for r in (d.window, d.page_size)]
+            ring = mem[: 2 * d.max_seqs * d.n_swa_layers * d.n_kv_heads * blk[0]]
+            pages = mem[swa: swa + 2 * d.n_full_layers * d.pages_per_full_layer * d.n_kv_heads * blk[1]]
+            return (ring.view(2, d.max_seqs, d.n_swa_layers, d.n_kv_heads, blk[0]),
+                    pages.view(2, d.n_full_layers, d.pages_per_full_layer, d.n_kv_heads, blk[1]))
         e = 1 if d.fp8 else 2
         ring_half = d.max_seqs * d.n_swa_layers * d.n_kv_heads * d.window * d.head_dim
         page_half = d.n_full_layers * d.pages_per_full_layer * d.n_kv_heads * d.page_size * d.head_dim
-        mem = self.memory
         ring = mem[: 2 * e * ring_half]
         pages = mem[swa: swa + 2 * e * page_half]
         if not d.fp8:
@@ -193,13 +218,15 @@ class KVPool:
     @property
     def ring(self) -> torch.Tensor:
         """[2 (K,V)][max_seqs][n_swa_layers][Hkv][W][d] view of the rolling buffers (bf16, or uint8
-        E4M3 codes in an FP8 pool)."""
+        E4M3 codes in an FP8 pool). A 4-bit pool gives its blocks as bytes, [2][max_seqs][n_swa_layers]
+        [Hkv][W * d / 2 code bytes, then W (step, minimum) bf16 pairs, padded to 16 bytes]."""
         return self._views()[0]
 
     @property
     def pages(self) -> torch.Tensor:
         """[2 (K,V)][n_full_layers][pages][Hkv][page_size][d] view of the paged pool (bf16, or uint8
-        E4M3 codes in an FP8 pool)."""
+        E4M3 codes in an FP8 pool). A 4-bit pool gives its blocks as bytes, [2][n_full_layers][pages]
+        [Hkv][page_size * d / 2 code bytes, then page_size (step, minimum) bf16 pairs]."""
         return self._views()[1]
 
     def set_scales(self, layer: int, k_scale, v_scale):
@@ -255,6 +282,95 @@ def kv_pool_append(pool: KVPool, layer: int, k: torch.Tensor, v: torch.Tensor, s
         pool.handle, layer, n_seqs, _ptr(seq_ids, torch.int32, "seq_ids"), _ptr(start_pos, torch.int64, "start_pos"),
         n_tok, _ptr(k, torch.bfloat16, "k"), _ptr(v, torch.bfloat16, "v"),
         _ptr(page_table, torch.int32, "page_table"), pt_stride, _stream(stream)))
+
+
+@dataclass(frozen=True)
+class RopeDesc:
+    """Rotary positions over up to four axes (hswa_rope_desc). inv_freq[i] (radians per position) and
+    axis[i] of pair i; rot_dim = 2 * len(inv_freq). interleaved: pairs (2i, 2i + 1) instead of
+    (i, i + rot_dim / 2)."""
+    inv_freq: tuple
+    axis: tuple | None = None
+    n_axes: int = 1
+    interleaved: bool = False
+
+    def c(self) -> RopeDescC:
+        c = self.__dict__.get("_c")
+        if c is None:
+            n = len(self.inv_freq)
+            axis = self.axis if self.axis is not None else [0] * n
+            if n > 64 or len(axis) != n or any(not 0 <= int(a) < 256 for a in axis):
+                raise ValueError("one axis per frequency, at most 64 frequencies")
+            c = RopeDescC(2 * n, self.n_axes, int(self.interleaved), 0, (ctypes.c_double * 64)(*map(float, self.inv_freq)),
+                          (ctypes.c_uint8 * 64)(*map(int, axis)))
+            object.__setattr__(self, "_c", c)
+        return c
+
+
+@dataclass(frozen=True)
+class ScoreMod:
+    """Changes to scores and visible keys (hswa_score_mod): capped scores, a distance bias per query head
+    (float32 [Hq]) and the range of keys each query sees (int64 [B, n_q], like the query rows)."""
+    softcap: float = 0.0
+    dist_slope: torch.Tensor | None = None
+    key_begin: torch.Tensor | None = None
+    key_end: torch.Tensor | None = None
+
+    def c(self, rows: tuple, n_q_heads: int) -> ScoreModC:
+        for name, t in (("key_begin", self.key_begin), ("key_end", self.key_end)):
+            if t is not None and tuple(t.shape) != tuple(rows):
+                raise ValueError(f"{name} must have one entry per query row {tuple(rows)}, got {tuple(t.shape)}")
+        if self.dist_slope is not None and self.dist_slope.numel() != n_q_heads:
+            raise ValueError("dist_slope must have one entry per query head")
+        return ScoreModC(self.softcap, _ptr(self.dist_slope, torch.float32, "dist_slope"),
+                         _ptr(self.key_begin, torch.int64, "key_begin"), _ptr(self.key_end, torch.int64, "key_end"))
+
+
+def rope_fwd(rope: RopeDesc, q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor, q_out: torch.Tensor | None = None,
+             k_out: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Rotate q [..., Hq, d] and k [..., Hkv, d] of the same tokens by their positions pos
+    [n_axes, tokens] (int64). q_out / k_out may be q / k."""
+    n = q.numel() // (q.shape[-1] * q.shape[-2]) if q.numel() else 0
+    if q.shape[:-2] != k.shape[:-2] or q.shape[-1] != k.shape[-1]:
+        raise ValueError("q and k must have the same tokens and head_dim")
+    if pos.shape[0] != rope.n_axes or pos.numel() != rope.n_axes * n:
+        raise ValueError(f"pos must be [n_axes, tokens] = [{rope.n_axes}, {n}], got {tuple(pos.shape)}")
+    q_out = torch.empty_like(q) if q_out is None else q_out
+    k_out = torch.empty_like(k) if k_out is None else k_out
+    if q_out.shape != q.shape or k_out.shape != k.shape:
+        raise ValueError("q_out and k_out must have the shapes of q and k")
+    _check(load_library().rope_fwd(
+        ctypes.byref(rope.c()), q.shape[-1], n, _ptr(pos, torch.int64, "pos"), _ptr(q, torch.bfloat16, "q"),
+        _ptr(q_out, torch.bfloat16, "q_out"), q.shape[-2], _ptr(k, torch.bfloat16, "k"),
+        _ptr(k_out, torch.bfloat16, "k_out"), k.shape[-2], _stream(stream)))
+    return q_out, k_out
+
+
+def kv_pool_append_rope(pool: KVPool, layer: int, rope: RopeDesc, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                        pos: torch.Tensor, start_pos: torch.Tensor, seq_ids: torch.Tensor | None = None,
+                        page_table: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
+                        k_out: torch.Tensor | None = None, keys_out: bool = True,
+                        stream=None) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """Rotate q [n_seqs, n_tok, Hq, d] and k [n_seqs, n_tok, Hkv, d] and commit the rotated keys and v
+    into layer ``layer`` in one pass. keys_out False: the rotated keys go to the pool only."""
+    n_seqs, n_tok = k.shape[0], k.shape[1]
+    d, hkv = pool.desc.head_dim, pool.desc.n_kv_heads
+    if tuple(k.shape) != (n_seqs, n_tok, hkv, d) or v.shape != k.shape or \
+            tuple(q.shape) != (n_seqs, n_tok, q.shape[-2], d):
+        raise ValueError("q, k, v must be [n_seqs, n_tok, heads, head_dim] of the pool")
+    if pos.shape[0] != rope.n_axes or pos.numel() != rope.n_axes * n_seqs * n_tok:
+        raise ValueError(f"pos must be [n_axes, tokens] = [{rope.n_axes}, {n_seqs * n_tok}], got {tuple(pos.shape)}")
+    q_out = torch.empty_like(q) if q_out is None else q_out
+    if k_out is None and keys_out:
+        k_out = torch.empty_like(k)
+    pt_stride = page_table.shape[1] if page_table is not None else 0
+    _check(load_library().kv_pool_append_rope(
+        pool.handle, layer, ctypes.byref(rope.c()), _ptr(pos, torch.int64, "pos"), n_seqs,
+        _ptr(seq_ids, torch.int32, "seq_ids"), _ptr(start_pos, torch.int64, "start_pos"), n_tok,
+        _ptr(q, torch.bfloat16, "q"), _ptr(q_out, torch.bfloat16, "q_out"), q.shape[2], _ptr(k, torch.bfloat16, "k"),
+        _ptr(k_out, torch.bfloat16, "k_out"), _ptr(v, torch.bfloat16, "v"),
+        _ptr(page_table, torch.int32, "page_table"), pt_stride, _stream(stream)))
+    return q_out, k_out
 
 
 def kv_pool_gather_ring(pool: KVPool, layer: int, dst_seq: int, src_seq: torch.Tensor, stream=None):
@@ -315,6 +431,25 @@ def hybrid_decode_fwd(pool: KVPool, layer: int, q: torch.Tensor, k_new: torch.Te
         _ptr(ctx_len, torch.int64, "ctx_len"), max_ctx_len, _ptr(seq_ids, torch.int32, "seq_ids"),
         _ptr(page_table, torch.int32, "page_table"), pt_stride, hq, _ptr(workspace, torch.uint8, "workspace"),
         workspace.numel(), _stream(stream)))
+    return o
+
+
+def hybrid_decode_mod_fwd(pool: KVPool, layer: int, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                          ctx_len: torch.Tensor, max_ctx_len: int, mod: ScoreMod, workspace: torch.Tensor,
+                          seq_ids: torch.Tensor | None = None, page_table: torch.Tensor | None = None,
+                          o: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """hybrid_decode_fwd with modified scores (capped, distance bias, key ranges [n_seqs, n_qt])."""
+    n_seqs, n_qt, hq, _ = q.shape
+    if o is None:
+        o = torch.empty_like(q)
+    pt_stride = page_table.shape[1] if page_table is not None else 0
+    m = mod.c((n_seqs, n_qt), hq)
+    _check(load_library().hybrid_decode_mod_fwd(
+        pool.handle, layer, _ptr(q, torch.bfloat16, "q"), _ptr(k_new, torch.bfloat16, "k_new"),
+        _ptr(v_new, torch.bfloat16, "v_new"), _ptr(o, torch.bfloat16, "o"), n_seqs, n_qt,
+        _ptr(ctx_len, torch.int64, "ctx_len"), max_ctx_len, _ptr(seq_ids, torch.int32, "seq_ids"),
+        _ptr(page_table, torch.int32, "page_table"), pt_stride, hq, ctypes.byref(m),
+        _ptr(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream)))
     return o
 
 

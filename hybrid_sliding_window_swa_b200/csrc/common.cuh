@@ -311,6 +311,13 @@ __device__ __forceinline__ uint16_t pack_e4m3x2(float lo, float hi) {
   return r;
 }
 
+// A capped score in the log2 domain: cap tanh(z / cap) log2 e, with in = 2 log2(e) / cap and
+// out = cap log2 e. tanh(u) = 1 - 2 / (1 + e^2u) has an absolute error of a few 2^-24 for every u
+// (infinite e^2u included), which is what a score needs.
+__device__ __forceinline__ float capped_log2(float z, float in, float out) {
+  return fmaf(-out, __fdividef(2.f, 1.f + ex2_approx(z * in)), out);
+}
+
 // ---------------------------------------------------------------- packed fp32x2 (sm_100)
 
 __device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {

@@ -25,6 +25,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "kv_quant.cuh"
 
 namespace hswa {
 
@@ -112,6 +113,14 @@ struct DecParams {
   uint8_t* ws;
   size_t part_off, part_bytes;
   int* err;
+  // extended launches (4-bit pools, score modifications)
+  int split;               // cached keys per split
+  int64_t blk_bytes;       // bytes of a ring block
+  float scale_nat;         // softmax scale without log2 e
+  float softcap, cap_in, cap_log2;
+  const float* slope;        // [Hq] distance slopes, or null
+  const int64_t* key_begin;  // [n_seqs][n_qt], or null
+  const int64_t* key_end;    // [n_seqs][n_qt], or null (causal)
 };
 
 __device__ __forceinline__ int64_t dec_klo(const DecParams& p, int64_t L) {
@@ -135,20 +144,80 @@ __device__ __forceinline__ int64_t safe_len(const DecParams& p, int s) {
   return L;
 }
 
+// Extended launches: positions row t of sequence s may see, [lo, hi), within [0, L + n_qt) and (SWA)
+// within the window on both sides. hi <= lo: nothing.
+__device__ __forceinline__ void row_range(const DecParams& p, int s, int64_t L, int t, int& lo, int& hi) {
+  const int64_t i = L + t;
+  int64_t a = 0, b = i + 1;
+  if (p.key_end) b = min(p.key_end[(int64_t)s * p.n_qt + t], L + p.n_qt);
+  if (p.key_begin) a = max(p.key_begin[(int64_t)s * p.n_qt + t], (int64_t)0);
+  if (p.window > 0) {
+    a = max(a, i - p.window + 1);
+    b = min(b, i + p.window);
+  }
+  b = max(b, (int64_t)0);
+  if (a > b) a = b;
+  lo = (int)a;
+  hi = (int)b;
+}
+
+// Cached keys a sequence's rows may need: [lo, hi). Extended launches cut it to the union of the rows'
+// ranges (pages: down to a page boundary).
+template <bool EXT>
+__device__ __forceinline__ void cached_range(const DecParams& p, int s, int64_t L, int64_t& lo, int64_t& hi) {
+  lo = dec_klo(p, L);
+  hi = L;
+  if constexpr (EXT) {
+    if (p.key_begin || p.key_end) {
+      int a = 0x7fffffff, b = 0;
+      for (int t = 0; t < p.n_qt; ++t) {
+        int rl, rh;
+        row_range(p, s, L, t, rl, rh);
+        if (rh > rl) {
+          a = min(a, rl);
+          b = max(b, rh);
+        }
+      }
+      lo = max(lo, (int64_t)a);
+      hi = min(hi, (int64_t)b);
+      if (lo > hi) lo = hi;
+    }
+    if (p.window <= 0) lo &= ~(int64_t)63;
+  }
+}
+
+template <bool EXT>
+__device__ __forceinline__ int split_len(const DecParams& p) {
+  return EXT ? p.split : SPLIT;
+}
+
+template <bool EXT>
+__device__ __forceinline__ int n_splits_x(const DecParams& p, int s, int64_t L) {
+  if constexpr (!EXT) return n_splits(p, L);
+  int64_t lo, hi;
+  cached_range<EXT>(p, s, L, lo, hi);
+  const int64_t n = (hi - lo + p.split - 1) / p.split;
+  return n < 1 ? 1 : (int)n;
+}
+
 // Length bucket of a sequence (part A order: higher first).
 __device__ __forceinline__ int class_a(int64_t L) { return L >= 262144 ? 2 : (L >= 65536 ? 1 : 0); }
 
 // Size class of a sequence's last split (part B order: higher first).
-__device__ __forceinline__ int class_b(const DecParams& p, int64_t L) {
-  const int64_t cached = L - dec_klo(p, L);
-  const int64_t tail = cached - (int64_t)(n_splits(p, L) - 1) * SPLIT;  // 0 .. SPLIT
-  const int c = (int)(tail / (SPLIT / NCLS_B));
+template <bool EXT>
+__device__ __forceinline__ int class_b(const DecParams& p, int s, int64_t L) {
+  int64_t lo, hi;
+  cached_range<EXT>(p, s, L, lo, hi);
+  const int split = split_len<EXT>(p);
+  const int64_t tail = hi - lo - (int64_t)(n_splits_x<EXT>(p, s, L) - 1) * split;  // 0 .. split
+  const int c = (int)(tail / (split / NCLS_B));
   return c < NCLS_B - 1 ? c : NCLS_B - 1;
 }
 
 // Builds the work list (see PlanView) and resets the work counter. One block of 1024 threads:
 // class totals, then a stable placement chunk by chunk (warp ballots give each thread its rank
 // among earlier threads of its class), then prefix sums of the body splits in part-A order.
+template <bool EXT>
 __global__ void __launch_bounds__(1024) plan_kernel(DecParams p) {
   WsHeader* hdr = reinterpret_cast<WsHeader*>(p.ws);
   PlanView pv(p.ws, p.n_seqs);
@@ -167,7 +236,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(DecParams p) {
     if (s < p.n_seqs) {
       const int64_t L = safe_len(p, s);
       atomicAdd(&cnt[class_a(L)], 1);
-      atomicAdd(&cnt[NCLS_A + class_b(p, L)], 1);
+      atomicAdd(&cnt[NCLS_A + class_b<EXT>(p, s, L)], 1);
     }
   }
   __syncthreads();
@@ -192,7 +261,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(DecParams p) {
     if (live) {
       const int64_t L = safe_len(p, s);
       ca = class_a(L);
-      cb = NCLS_A + class_b(p, L);
+      cb = NCLS_A + class_b<EXT>(p, s, L);
     }
     int rank_a = 0, rank_b = 0;
 #pragma unroll
@@ -232,7 +301,11 @@ __global__ void __launch_bounds__(1024) plan_kernel(DecParams p) {
   __syncthreads();
   for (int base = 0; base < p.n_seqs; base += 1024) {
     const int pos = base + tid;
-    const int v = pos < p.n_seqs ? n_splits(p, safe_len(p, pv.order[pos])) - 1 : 0;
+    int v = 0;
+    if (pos < p.n_seqs) {
+      const int s = pv.order[pos];
+      v = n_splits_x<EXT>(p, s, safe_len(p, s)) - 1;
+    }
     int x = v;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -350,7 +423,11 @@ struct DecSmem {
 //  * The K scale of the KV head multiplies the softmax scale; the V scale multiplies O. The new
 //    tokens are quantized with the layer's reciprocal scales as they are staged, the values the
 //    cache holds once they are committed.
-template <int D, int MT, bool FP8>
+//
+// EXT: splits of p.split keys, per-row key ranges, capped scores and a distance bias (row_range; the
+// ranges replace the causal bound, the scores take cap tanh(s / cap) - slope |i - j|). Keys no row
+// sees are filled with zeros or masked, and a row that sees nothing gives zeros.
+template <int D, int MT, bool FP8, bool EXT>
 __global__ void __launch_bounds__(DEC_THREADS, 2) decode_kernel(DecParams p) {
   using SM = DecSmem<D, MT, FP8>;
   constexpr int ROWS = SM::ROWS;
@@ -400,13 +477,25 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) decode_kernel(DecParams p) {
       c = -1;
     }
     const int L = (int)safe_len(p, s);
-    const int nsp = n_splits(p, L);
+    const int nsp = n_splits_x<EXT>(p, s, L);
     if (c < 0) c = nsp - 1;
     const bool last = c == nsp - 1;
-    const int klo = (int)dec_klo(p, L);
-    const int a = klo + c * SPLIT;
-    const int b = (a + SPLIT < L) ? a + SPLIT : L;
+    int64_t klo64, khi64;
+    cached_range<EXT>(p, s, L, klo64, khi64);
+    const int klo = (int)klo64, khi = (int)khi64;
+    const int split = split_len<EXT>(p);
+    const int a = klo + c * split;
+    const int b = (a + split < khi) ? a + split : khi;
     const int n_cached_blk = (b - a + KB - 1) / KB;
+    int lo_all = 0;  // EXT: rows of a page below every row's range are not read
+    if constexpr (EXT) {
+      lo_all = 0x7fffffff;
+      for (int t = 0; t < p.n_qt; ++t) {
+        int rl, rh;
+        row_range(p, s, L, t, rl, rh);
+        if (rh > rl) lo_all = min(lo_all, rl);
+      }
+    }
     const int n_blk = n_cached_blk + (last ? 1 : 0);
     // source rows of this (sequence, KV head), as bytes
     constexpr int RB = FP8 ? D : 2 * D;  // bytes per K/V row
@@ -464,7 +553,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) decode_kernel(DecParams p) {
 #pragma unroll
           for (int rr = 0; rr < KB; rr += CP_ROWS) {
             const int r = rr + cp_row;
-            const bool ok = ok_page && r < nvalid;
+            const bool ok = ok_page && r < nvalid && (!EXT || pos0 + r >= lo_all);
             const int off = ok ? r * RB + cp_chunk * 16 : 0;
             cp_async_16(kdst + kv_off(r, cp_chunk), ok ? kbase + off : p.src_k8, ok ? 16u : 0u);
             cp_async_16(vdst + kv_off(r, cp_chunk), ok ? vbase + off : p.src_v8, ok ? 16u : 0u);
@@ -566,6 +655,9 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) decode_kernel(DecParams p) {
     float o_acc[MT][D / 8][4];
     float m_r[MT][2], l_r[MT][2];
     int row_pos[MT][2], row_lo[MT][2];
+    int row_hi[MT][2];     // EXT: end of the row's range
+    float row_sl[MT][2];   // EXT: distance slope times log2 e
+    int ext_lo = 0, ext_hi = 0x7fffffff;  // EXT: every row sees [ext_lo, ext_hi)
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
@@ -581,6 +673,13 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) decode_kernel(DecParams p) {
           if (lo2 < 0) lo2 = 0;
         }
         row_lo[mt][hf] = r < p.R ? lo2 : 0x7fffffff;  // padding rows see nothing
+        if constexpr (EXT) {
+          int rl, rh;
+          row_range(p, s, L, t, rl, rh);
+          row_lo[mt][hf] = r < p.R ? rl : 0x7fffffff;
+          row_hi[mt][hf] = rh;
+          row_sl[mt][hf] = p.slope && r < p.R ? p.slope[g * p.G + r % p.G] * 1.4426950408889634f : 0.f;
+        }
       }
 #pragma unroll
       for (int nd = 0; nd < D / 8; ++nd) o_acc[mt][nd][0] = o_acc[mt][nd][1] = o_acc[mt][nd][2] = o_acc[mt][nd][3] = 0.f;
@@ -588,7 +687,16 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) decode_kernel(DecParams p) {
     // largest window start over the real rows: cached keys at or above it need no mask
     const int lo_max = p.window > 0 ? (L + p.n_qt - 1 - p.window + 1 > 0 ? L + p.n_qt - p.window : 0) : 0;
 
-    const float sl2 = FP8 ? p.scale_log2 * p.k_scale[g] : p.scale_log2;
+    if constexpr (EXT) {
+      for (int t = 0; t < p.n_qt; ++t) {
+        int rl, rh;
+        row_range(p, s, L, t, rl, rh);
+        ext_lo = max(ext_lo, rl);
+        ext_hi = min(ext_hi, rh);
+      }
+    }
+
+    const float sl2 = (EXT ? p.scale_nat : p.scale_log2) * (FP8 ? p.k_scale[g] : 1.f);
     for (int kb2 = 0; kb2 < n_blk; ++kb2) {
       asm volatile("cp.async.wait_group %0;" ::"n"(NS - 2) : "memory");
       __syncthreads();  // block kb2 is visible; every warp is done with block kb2 - 1
@@ -658,7 +766,8 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) decode_kernel(DecParams p) {
       // mask (edge blocks only) + online softmax in the exp2 domain with lazy rescaling
       const bool is_new = kb2 >= n_cached_blk;
       const int kpos_base = is_new ? L : a + kb2 * KB;
-      const bool need_mask = is_new || kpos_base + KB > b || kpos_base < lo_max;
+      const bool need_mask = EXT ? is_new || kpos_base + KB > min(b, ext_hi) || kpos_base < ext_lo
+                                 : is_new || kpos_base + KB > b || kpos_base < lo_max;
       uint32_t pa[MT][4];
       // this lane's key columns are key0 + (lane & 3) * 2 + {0, 1, 8, 9}
       const int col_base = kpos_base + key0 + (lane & 3) * 2;
@@ -670,7 +779,18 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) decode_kernel(DecParams p) {
           // exponential's FMA (max(s) * c = max(s * c) exactly, rounding being monotone; measured 2%
           // faster there); bf16 blocks: scaled scores (the other form measured 1.6% slower there)
           float v[4];
-          if constexpr (FP8) {
+          if constexpr (EXT) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int key = col_base + (x >> 1) * 8 + (x & 1);
+              float z = sacc[mt][x >> 1][hf * 2 + (x & 1)] * sl2;
+              z = p.softcap > 0.f ? capped_log2(z, p.cap_in, p.cap_log2) : z * 1.4426950408889634f;
+              if (p.slope) z = fmaf(-row_sl[mt][hf], (float)abs(row_pos[mt][hf] - key), z);
+              if (need_mask && (key < row_lo[mt][hf] || key >= row_hi[mt][hf] || key >= (is_new ? L + p.n_qt : b)))
+                z = -INFINITY;
+              v[x] = z;
+            }
+          } else if constexpr (FP8) {
             v[0] = sacc[mt][0][hf * 2 + 0];
             v[1] = sacc[mt][0][hf * 2 + 1];
             v[2] = sacc[mt][1][hf * 2 + 0];
@@ -706,7 +826,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) decode_kernel(DecParams p) {
           float mx = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          if constexpr (FP8) mx *= sl2;
+          if constexpr (FP8 && !EXT) mx *= sl2;
           // lazy rescale: move the offset only when the maximum grew by more than 2^8
           if (mx > m_r[mt][hf] + 8.f) {
             const float alpha = ex2_approx(m_r[mt][hf] - mx);  // 0 when the old offset is -inf
@@ -721,7 +841,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) decode_kernel(DecParams p) {
           const float moff = m_r[mt][hf] == -INFINITY ? 0.f : m_r[mt][hf];
           float pv[4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) pv[x] = FP8 ? ex2_approx(fmaf(v[x], sl2, -moff)) : ex2_approx(v[x] - moff);
+          for (int x = 0; x < 4; ++x) pv[x] = FP8 && !EXT ? ex2_approx(fmaf(v[x], sl2, -moff)) : ex2_approx(v[x] - moff);
           l_r[mt][hf] += (pv[0] + pv[1]) + (pv[2] + pv[3]);
           // A fragment of P (16 rows x 16 keys): a0/a1 = keys 0-7 (rows r, r+8), a2/a3 = keys 8-15
           if constexpr (FP8) {
@@ -849,7 +969,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) decode_kernel(DecParams p) {
       // single split: normalise and write bf16 output rows
       for (int idx = tid; idx < p.R * (D / 8); idx += DEC_THREADS) {
         const int r = idx / (D / 8), ch = idx % (D / 8);
-        const float inv = vs / l_all[r];
+        const float inv = EXT && l_all[r] == 0.f ? 0.f : vs / l_all[r];
         const float4 lo4 = merged4(r, ch * 8), hi4 = merged4(r, ch * 8 + 4);
         uint4 pk;
         pk.x = pack_bf16x2(lo4.x * inv, lo4.y * inv);
@@ -884,13 +1004,13 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) decode_kernel(DecParams p) {
 //           (shuffles within the 8-thread group), keeping the factors 2^(m_c - M) in shared memory;
 //  phase 2: each thread owns 4 float4 groups of the R x D output and walks the splits with
 //           8 independent loads in flight.
-template <int D>
+template <int D, bool EXT>
 __global__ void __launch_bounds__(256) merge_kernel(DecParams p) {
   const int g = blockIdx.x % p.Hkv;
   const int s = blockIdx.x / p.Hkv;
   const WsHeader* hdr = reinterpret_cast<const WsHeader*>(p.ws);
   const PlanView pv(p.ws, p.n_seqs);
-  const int nsp = n_splits(p, safe_len(p, s));
+  const int nsp = n_splits_x<EXT>(p, s, safe_len(p, s));
   if (nsp <= 1) return;
   extern __shared__ float msh[];  // [nsp][R] scale factors, then [R] inverse denominators
   float* fac = msh;
@@ -924,7 +1044,7 @@ __global__ void __launch_bounds__(256) merge_kernel(DecParams p) {
     den += __shfl_xor_sync(0xffffffffu, den, 1);
     den += __shfl_xor_sync(0xffffffffu, den, 2);
     den += __shfl_xor_sync(0xffffffffu, den, 4);
-    if (live && lane8 == 0) inv[r] = 1.f / den;
+    if (live && lane8 == 0) inv[r] = EXT && den == 0.f ? 0.f : 1.f / den;
   }
   __syncthreads();
   constexpr int Q4 = D / 4;  // float4 groups per row
@@ -988,28 +1108,64 @@ __global__ void __launch_bounds__(256) merge_kernel(DecParams p) {
 }
 
 #include "decode_tc.cuh"
+#include "decode_i4.cuh"
 
 // Largest split count of any sequence for these arguments.
-int64_t max_splits(int window, int64_t max_ctx_len) {
+int64_t max_splits(int window, int64_t max_ctx_len, int split = SPLIT) {
   const int64_t cached = window > 0 ? (max_ctx_len < window ? max_ctx_len : window - 1) : max_ctx_len;
-  const int64_t nsp = (cached + SPLIT - 1) / SPLIT;
+  const int64_t nsp = (cached + split - 1) / split;
   return nsp < 1 ? 1 : nsp;
 }
 
-template <int D, int MT, bool FP8>
+// Keys per split of an extended launch. Long enough that the merge is small against the reads (8192, as
+// in the other launches), shorter when the sequences would not fill the CTAs otherwise: about
+// kSplitItems work items over all (sequence, KV head) pairs if every context has the maximum length.
+constexpr int64_t kSplitItems = 592;  // two items for each of 148 x 2 resident CTAs
+int ext_split(int n_seqs, int Hkv, int window, int64_t max_ctx_len) {
+  const int64_t cached = window > 0 && max_ctx_len > window ? window : max_ctx_len;
+  const int64_t pairs = (int64_t)n_seqs * Hkv;
+  const int64_t want = pairs > 0 ? (kSplitItems + pairs - 1) / pairs : 1;
+  int64_t split = (cached + want - 1) / want;
+  split = (split + 63) / 64 * 64;
+  return (int)(split < 256 ? 256 : (split > SPLIT ? SPLIT : split));
+}
+
+template <int D, int MT, bool FP8, bool EXT>
 int launch_t(DecParams& p, int n_items_max, int sms, size_t merge_smem, cudaStream_t stream) {
   using SM = DecSmem<D, MT, FP8>;
-  plan_kernel<<<1, 1024, 0, stream>>>(p);
-  cudaFuncSetAttribute(decode_kernel<D, MT, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::BYTES);
+  plan_kernel<EXT><<<1, 1024, 0, stream>>>(p);
+  cudaFuncSetAttribute(decode_kernel<D, MT, FP8, EXT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::BYTES);
   int per_sm = 2;
   int grid = sms * per_sm;
   if (grid > n_items_max) grid = n_items_max;
   if (grid < 1) grid = 1;
-  decode_kernel<D, MT, FP8><<<grid, DEC_THREADS, SM::BYTES, stream>>>(p);
+  decode_kernel<D, MT, FP8, EXT><<<grid, DEC_THREADS, SM::BYTES, stream>>>(p);
   if (merge_smem > 0) {
     if (merge_smem > 48 * 1024)
-      cudaFuncSetAttribute(merge_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)merge_smem);
-    merge_kernel<D><<<p.n_seqs * p.Hkv, 256, merge_smem, stream>>>(p);
+      cudaFuncSetAttribute(merge_kernel<D, EXT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)merge_smem);
+    merge_kernel<D, EXT><<<p.n_seqs * p.Hkv, 256, merge_smem, stream>>>(p);
+  }
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) {
+    set_error("hybrid_decode_fwd: launch failed: %s", cudaGetErrorString(e));
+    return HSWA_ERR_CUDA;
+  }
+  return HSWA_OK;
+}
+
+template <int D, int NT, int RG, bool MOD>
+int launch_i4(DecParams& p, int n_items_max, int sms, size_t merge_smem, cudaStream_t stream) {
+  using SM = I4Smem<D, NT, RG>;
+  plan_kernel<true><<<1, 1024, 0, stream>>>(p);
+  cudaFuncSetAttribute(decode_i4_kernel<D, NT, RG, MOD>, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::BYTES);
+  int grid = sms * 2;
+  if (grid > n_items_max) grid = n_items_max;
+  if (grid < 1) grid = 1;
+  decode_i4_kernel<D, NT, RG, MOD><<<grid, I4_THREADS, SM::BYTES, stream>>>(p);
+  if (merge_smem > 0) {
+    if (merge_smem > 48 * 1024)
+      cudaFuncSetAttribute(merge_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)merge_smem);
+    merge_kernel<D, true><<<p.n_seqs * p.Hkv, 256, merge_smem, stream>>>(p);
   }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {
@@ -1020,7 +1176,7 @@ int launch_t(DecParams& p, int n_items_max, int sms, size_t merge_smem, cudaStre
 }
 
 int launch_tc(DecParams& p, int n_items_max, int sms, size_t merge_smem, cudaStream_t stream) {
-  plan_kernel<<<1, 1024, 0, stream>>>(p);
+  plan_kernel<false><<<1, 1024, 0, stream>>>(p);
   const int smem = TcLayout::BYTES + 1024;
   cudaFuncSetAttribute(decode_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   int grid = sms < n_items_max ? sms : n_items_max;
@@ -1028,8 +1184,8 @@ int launch_tc(DecParams& p, int n_items_max, int sms, size_t merge_smem, cudaStr
   decode_tc_kernel<<<grid, TC_THREADS, smem, stream>>>(p);
   if (merge_smem > 0) {
     if (merge_smem > 48 * 1024)
-      cudaFuncSetAttribute(merge_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)merge_smem);
-    merge_kernel<128><<<p.n_seqs * p.Hkv, 256, merge_smem, stream>>>(p);
+      cudaFuncSetAttribute(merge_kernel<128, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)merge_smem);
+    merge_kernel<128, false><<<p.n_seqs * p.Hkv, 256, merge_smem, stream>>>(p);
   }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {
@@ -1041,16 +1197,17 @@ int launch_tc(DecParams& p, int n_items_max, int sms, size_t merge_smem, cudaStr
 
 }  // namespace
 
-size_t decode_workspace_bytes(int n_seqs, int n_qt, int Hq, int Hkv, int d, int window, int64_t max_ctx_len) {
+size_t decode_workspace_bytes(int n_seqs, int n_qt, int Hq, int Hkv, int d, int window, int64_t max_ctx_len,
+                              bool ext) {
   const int G = Hq / Hkv;
   const int rows = n_qt * G;
-  WsLayout L(n_seqs, rows, d, (int64_t)n_seqs * Hkv * max_splits(window, max_ctx_len));
+  const int split = ext ? ext_split(n_seqs, Hkv, window, max_ctx_len) : SPLIT;
+  WsLayout L(n_seqs, rows, d, (int64_t)n_seqs * Hkv * max_splits(window, max_ctx_len, split));
   return L.bytes;
 }
 
-size_t decode_merge_smem_bytes(int n_seqs, int n_qt, int Hq, int Hkv, int window, int64_t max_ctx_len) {
-  (void)n_seqs;
-  const int64_t nsp = max_splits(window, max_ctx_len);
+size_t decode_merge_smem_bytes(int n_seqs, int n_qt, int Hq, int Hkv, int window, int64_t max_ctx_len, bool ext) {
+  const int64_t nsp = max_splits(window, max_ctx_len, ext ? ext_split(n_seqs, Hkv, window, max_ctx_len) : SPLIT);
   if (nsp <= 1) return 0;
   // [nsp][R] scale factors and [R] inverse denominators
   return (size_t)(nsp + 1) * (size_t)(n_qt * (Hq / Hkv)) * sizeof(float);
@@ -1095,7 +1252,20 @@ int launch_decode(const DecodeLaunch& Lc, cudaStream_t stream) {
   p.scale_log2 = (float)(1.4426950408889634 / sqrt((double)Lc.d));
   p.ws = static_cast<uint8_t*>(Lc.workspace);
   p.err = pool->err;
-  const int64_t mi = (int64_t)p.n_seqs * p.Hkv * max_splits(p.window, p.max_ctx_len);
+  p.split = Lc.ext ? ext_split(p.n_seqs, p.Hkv, p.window, p.max_ctx_len) : SPLIT;
+  p.blk_bytes = pool->ring_blk;
+  p.scale_nat = (float)(1.0 / sqrt((double)Lc.d));
+  if (Lc.mod) {
+    p.softcap = Lc.mod->softcap;
+    if (p.softcap > 0.f) {
+      p.cap_in = (float)(2.0 * 1.4426950408889634 / p.softcap);
+      p.cap_log2 = (float)(1.4426950408889634 * p.softcap);
+    }
+    p.slope = Lc.mod->dist_slope;
+    p.key_begin = Lc.mod->key_begin;
+    p.key_end = Lc.mod->key_end;
+  }
+  const int64_t mi = (int64_t)p.n_seqs * p.Hkv * max_splits(p.window, p.max_ctx_len, p.split);
   WsLayout WL(p.n_seqs, p.R, Lc.d, mi);
   p.part_off = WL.part_off;
   p.part_bytes = WL.part_bytes_per_item;
@@ -1105,8 +1275,27 @@ int launch_decode(const DecodeLaunch& Lc, cudaStream_t stream) {
     return HSWA_ERR_UNSUPPORTED_SHAPE;
   }
   const int nmax = mi > 0x7fffffff ? 0x7fffffff : (int)mi;
-  const size_t msm = decode_merge_smem_bytes(p.n_seqs, p.n_qt, p.Hq, p.Hkv, p.window, p.max_ctx_len);
+  const size_t msm = decode_merge_smem_bytes(p.n_seqs, p.n_qt, p.Hq, p.Hkv, p.window, p.max_ctx_len, Lc.ext);
   const int sms = pool->sms;
+  if (pool->i4) {
+#define HSWA_I4(DD, MODD)                                                              \
+  (p.R <= 8    ? launch_i4<DD, 1, 1, MODD>(p, nmax, sms, msm, stream)                  \
+   : p.R <= 16 ? launch_i4<DD, 2, 1, MODD>(p, nmax, sms, msm, stream)                  \
+               : launch_i4<DD, 2, 2, MODD>(p, nmax, sms, msm, stream))
+    if (Lc.d == 128) return Lc.mod ? HSWA_I4(128, true) : HSWA_I4(128, false);
+    return Lc.mod ? HSWA_I4(64, true) : HSWA_I4(64, false);
+#undef HSWA_I4
+  }
+  if (Lc.mod) {
+#define HSWA_DEC(DD, MM, F8) launch_t<DD, MM, F8, true>(p, nmax, sms, msm, stream)
+    if (pool->fp8) {
+      if (Lc.d == 128) return p.R <= 16 ? HSWA_DEC(128, 1, true) : HSWA_DEC(128, 2, true);
+      return p.R <= 16 ? HSWA_DEC(64, 1, true) : HSWA_DEC(64, 2, true);
+    }
+    if (Lc.d == 128) return p.R <= 16 ? HSWA_DEC(128, 1, false) : HSWA_DEC(128, 2, false);
+    return p.R <= 16 ? HSWA_DEC(64, 1, false) : HSWA_DEC(64, 2, false);
+#undef HSWA_DEC
+  }
   // FP8 pools with head_dim 128 may run the tcgen05 kernel of decode_tc.cuh instead of the mma.sync
   // one: environment variable HSWA_DECODE_TC = 1 (full layers) or 2 (every layer), read once per
   // process; unset or 0 keeps decode_kernel, the faster of the two as measured.
@@ -1116,7 +1305,7 @@ int launch_decode(const DecodeLaunch& Lc, cudaStream_t stream) {
   }();
   if (pool->fp8 && Lc.d == 128 && (tc_mode >= 2 || (tc_mode == 1 && p.window <= 0)))
     return launch_tc(p, nmax, sms, msm, stream);
-#define HSWA_DEC(DD, MM, F8) launch_t<DD, MM, F8>(p, nmax, sms, msm, stream)
+#define HSWA_DEC(DD, MM, F8) launch_t<DD, MM, F8, false>(p, nmax, sms, msm, stream)
   if (pool->fp8) {
     if (Lc.d == 128) return p.R <= 16 ? HSWA_DEC(128, 1, true) : HSWA_DEC(128, 2, true);
     return p.R <= 16 ? HSWA_DEC(64, 1, true) : HSWA_DEC(64, 2, true);
@@ -1173,7 +1362,7 @@ extern "C" int hybrid_decode_fwd_noalloc(hswa_pool* pool, int layer, const hswa_
   size_t need = 0;
   // the same argument checks as hybrid_decode_fwd (including that the pool's device is current)
   int rc = hswa::prepare_decode(pool, "hybrid_decode_fwd_noalloc", layer, q, k_new, v_new, o, n_seqs, n_q_per_seq,
-                                ctx_len, max_ctx_len, seq_ids, page_table, pt_stride, n_q_heads, &L, &need);
+                                ctx_len, max_ctx_len, seq_ids, page_table, pt_stride, n_q_heads, nullptr, &L, &need);
   if (rc || L.n_seqs == 0) return rc;
   if (need > (size_t)HSWA_NOALLOC_SCRATCH_BYTES) {
     hswa::set_error("hybrid_decode_fwd_noalloc: this call needs %zu bytes of scratch but the built-in array holds "

@@ -1,0 +1,731 @@
+// decode_i4.cuh -- the decode step over a 4-bit pool (included by decode.cu, which holds the work
+// list, the parameters and the merge of the splits).
+//
+// Math. A cached row stands for code * step + lo (kv_quant.cuh), so with k = step_k c + lo_k:
+//   q . k = step_k (q . c) + lo_k sum(q),      o = sum_j p_j v_j = sum_j (p_j step_j) c_j + sum_j p_j lo_j.
+// Both products therefore run on the codes themselves. An f16 with exponent field 0 is a subnormal:
+// its value is its mantissa times 2^-24. A code masked out of its word is such a number, code * 2^-24
+// for the low nibble of a byte and code * 2^-20 for the high one, without any conversion: five integer
+// instructions turn a 32-bit word of eight codes into four f16 pairs of an MMA operand. The two
+// factors are powers of two and are folded into Q (whose entries at odd dims are staged divided by 16)
+// and, for O, into the output.
+//
+// Orientation. S^T = K Q^T and O^T = V^T P^T with mma.sync m16n8k16: keys (and dims of V) fill the 16
+// rows, query rows come in groups of 8 columns, so a step of one token with 8 heads per KV head wastes
+// nothing. The codes go from shared memory to A fragments as they lie:
+//   K  lane (g, t) reads 16 bytes (D = 128) of key pi(g): 32 dims, whose order inside the dot product
+//      is free as long as Q is staged in the same order;
+//   V  lane (g, t) reads the bytes of its 16 dims (16 g ..) of keys t, 4 + t, 8 + t, 12 + t; two keys'
+//      words are interleaved by a byte permute, then masked. pi (the order of the 16 keys along S^T's
+//      rows) is chosen so that these are the keys 2t, 2t+1, 2t+8, 2t+9 of the P^T fragment, and both
+//      reads are free of bank conflicts.
+// P (times the key's V step) is rounded to f16 (11 bits; an fp32 sum keeps l and sum p lo) and turned
+// from accumulator to operand layout by movmatrix.
+// f16 range: Q is staged with its row maximum at 2^14 .. 2^15 and the factor kept in fp32. p is at most
+// 2^8 (lazy rescaling as in the other kernels) and the V steps are divided by a power of two that
+// brings the largest so far to 2^6 .. 2^7; a larger one raises it and rescales O. P keeps its 11 bits
+// down to 2^-20 of the largest p * step.
+//
+// What bounds it. 2 (d / 2 + 4) bytes per key and KV head against about 100 integer, 16 ldmatrix-free
+// shared loads and 16 MMAs per 16 keys and 8 rows. Bytes for up to 8 rows, the MMA rate for 32.
+//
+// Structure: 4 consumer warps and a producer warp per CTA, two CTAs per SM, taking items from the work
+// list. A block is one 64-key page: (codes, pairs) of K and of V are contiguous, one bulk copy each
+// (cp.async for ring rows, whose runs may start anywhere), several blocks ahead, across items. The
+// producer also hands over the item's geometry and its Q rows. Warps split a block's keys (and, for
+// more than 16 rows, the rows) and merge their softmax states at the end of the item.
+// Waits are bounded; a failing wait makes its warp return and the others run out theirs.
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Arrive on the barrier when this thread's cp.async copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// 2^e for -126 <= e <= 127.
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+
+constexpr int I4_WARPS = 4;  // consumer warps
+constexpr int I4_THREADS = (I4_WARPS + 1) * 32;
+
+// One work item as the producer hands it to the consumers.
+struct I4Item {
+  int item, s, g, L;
+  int a, b;              // cached keys [a, b) of this split
+  int n_cached, n_blk;   // blocks of cached keys, blocks with the new tokens
+  int nsp;               // splits of the sequence
+  int lo_min, lo_max;    // over the rows: smallest and largest first visible position
+  int hi_min;            // smallest end of the visible range
+  int row_lo[8], row_hi[8];  // per new token
+};
+
+template <int D, int NT, int RG>
+struct I4Smem {
+  static constexpr int ROWS = 8 * NT * RG;
+  static constexpr int BLK = (int)i4_block_bytes(64, D);
+  static constexpr int STAGE = 2 * BLK;
+  static constexpr int NS = (RG == 2 ? 6 : 9) * (D == 128 ? 1 : 2);
+  static constexpr int Q_BYTES = ROWS * D * 2;
+  static constexpr int AREA_STRIDE = D + 4;  // floats
+  static constexpr int Q_OFF = NS * STAGE;
+  static constexpr int AREA_OFF = Q_OFF + 2 * Q_BYTES;
+  static constexpr int ML_OFF = AREA_OFF + 2 * ROWS * AREA_STRIDE * 4;
+  // m, l, sum p lo per (warp, row); 2^E per warp; then m, 1/l or l, sum p lo per row
+  static constexpr int ITEM_OFF = ML_OFF + (3 * I4_WARPS * ROWS + I4_WARPS + 3 * ROWS) * 4;
+  static constexpr int BAR_OFF = (ITEM_OFF + 2 * (int)sizeof(I4Item) + 15) / 16 * 16;
+  static constexpr int BYTES = BAR_OFF + (2 * NS + 5) * 8 + 16;
+  static_assert(2 * (BYTES + 1024) <= 227 * 1024, "two CTAs per SM");
+};
+
+template <int D, int NT, int RG, bool MOD>
+__global__ void __launch_bounds__(I4_THREADS, 2) decode_i4_kernel(DecParams p) {
+  using SM = I4Smem<D, NT, RG>;
+  constexpr int ROWS = SM::ROWS;
+  constexpr int NS = SM::NS;
+  constexpr int KW = I4_WARPS / RG;    // warps that share a row group
+  constexpr int KG = RG;               // 16-key groups per warp and block: 64 / 16 / KW
+  constexpr int NW = D / 32;           // 32-bit words of K codes per lane
+  constexpr int MT = D / 16;           // m-tiles of O^T
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::BAR_OFF);
+  uint64_t* empty = full + NS;
+  uint64_t* item_full = empty + NS;
+  uint64_t* item_empty = item_full + 2;
+  uint64_t* cons = item_empty + 2;
+  int* go = reinterpret_cast<int*>(cons + 1);
+  I4Item* items = reinterpret_cast<I4Item*>(smem + SM::ITEM_OFF);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  WsHeader* hdr = reinterpret_cast<WsHeader*>(p.ws);
+
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&full[i], 33);  // the producer's 32 lanes and its byte count
+      mbar_init(&empty[i], I4_WARPS);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&item_full[i], 1);
+      mbar_init(&item_empty[i], I4_WARPS);
+    }
+    mbar_init(cons, I4_WARPS);
+    fence_barrier_init();
+    *go = read_error(p.err) == 0;
+  }
+  __syncthreads();
+  if (!*go) return;  // a pending device error: skip the work
+
+  if (warp == I4_WARPS) {
+    // ------------------------------------------------------------ producer
+    const PlanView pv(p.ws, p.n_seqs);
+    uint32_t cnt = 0;  // blocks issued
+    int it = 0;
+    bool ok = true;
+    for (;; ++it) {
+      const int slot = it & 1;
+      if (!(ok = warp_wait(&item_empty[slot], ((it >> 1) & 1) ^ 1, p.err))) break;
+      int item = 0;
+      if (lane == 0) item = atomicAdd(&hdr->counter, 1);
+      item = __shfl_sync(0xffffffffu, item, 0);
+      I4Item& I = items[slot];
+      if (item >= hdr->total_items) {
+        if (lane == 0) {
+          I.item = -1;
+          mbar_arrive(&item_full[slot]);
+        }
+        break;
+      }
+      const int g = item % p.Hkv;
+      const int sc = item / p.Hkv;
+      int s, c;
+      if (sc < hdr->body_total) {
+        int lo = 0, hi = p.n_seqs;
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (pv.prefix[mid] <= sc) lo = mid; else hi = mid;
+        }
+        s = pv.order[lo];
+        c = sc - pv.prefix[lo];
+      } else {
+        s = pv.tail[sc - hdr->body_total];
+        c = -1;
+      }
+      const int L = (int)safe_len(p, s);
+      int64_t klo64, khi64;
+      cached_range<true>(p, s, L, klo64, khi64);
+      const int klo = (int)klo64, khi = (int)khi64;
+      const int nsp = n_splits_x<true>(p, s, L);
+      if (c < 0) c = nsp - 1;
+      const int a = klo + c * p.split;
+      const int b = a + p.split < khi ? a + p.split : khi;
+      const int n_cached = b > a ? (b - a + 63) / 64 : 0;
+      const int n_blk = n_cached + (c == nsp - 1 ? 1 : 0);
+      // visible range of each new token's rows, by lane
+      int rlo = 0, rhi = 0x7fffffff;
+      row_range(p, s, L, lane < p.n_qt ? lane : 0, rlo, rhi);
+      int lo_min = rhi > rlo ? rlo : 0x7fffffff, lo_max = rlo, hi_min = rhi;  // a row may see nothing
+#pragma unroll
+      for (int x = 1; x < 8; x <<= 1) {
+        lo_min = min(lo_min, __shfl_xor_sync(0xffffffffu, lo_min, x));
+        lo_max = max(lo_max, __shfl_xor_sync(0xffffffffu, lo_max, x));
+        hi_min = min(hi_min, __shfl_xor_sync(0xffffffffu, hi_min, x));
+      }
+      if (lane < 8) {
+        I.row_lo[lane] = rlo;
+        I.row_hi[lane] = rhi;
+      }
+      __syncwarp();
+      if (lane == 0) {
+        I.item = item;
+        I.s = s;
+        I.g = g;
+        I.L = L;
+        I.a = a;
+        I.b = b;
+        I.n_cached = n_cached;
+        I.n_blk = n_blk;
+        I.nsp = nsp;
+        I.lo_min = lo_min;
+        I.lo_max = lo_max;
+        I.hi_min = hi_min;
+        const uint32_t row_bytes = p.G * D * 2;
+        mbar_arrive_expect_tx(&item_full[slot], p.n_qt * row_bytes);
+        uint8_t* dst = smem + SM::Q_OFF + slot * SM::Q_BYTES;
+        for (int t = 0; t < p.n_qt; ++t)
+          bulk_load(dst + t * row_bytes, p.q + (((int64_t)s * p.n_qt + t) * p.Hq + g * p.G) * D, row_bytes,
+                    &item_full[slot]);
+      }
+      // sources
+      int64_t ring_block = -1;
+      if (p.window > 0 && n_cached > 0) {
+        const int seq = p.seq_ids[s];
+        if (seq < 0 || seq >= p.max_seqs) {
+          if (lane == 0) record_error(p.err, HSWA_ERR_DEVICE_BOUNDS);
+        } else {
+          ring_block = ((int64_t)seq * p.n_swa + p.ring_layer) * p.Hkv + g;
+        }
+      }
+      const int32_t* pt_row = p.page_table ? p.page_table + (int64_t)s * p.pt_stride : nullptr;
+      int my_page = -1;
+      for (int kb = 0; kb < n_blk; ++kb, ++cnt) {
+        const int st = cnt % NS;
+        if (p.window <= 0 && (kb & 31) == 0) {
+          const int lp = (a >> 6) + kb + lane;
+          my_page = kb + lane < n_cached && lp < p.pt_stride ? pt_row[lp] : -1;
+        }
+        if (!(ok = warp_wait(&empty[st], ((cnt / NS) & 1) ^ 1, p.err))) break;
+        uint8_t* ks = smem + st * SM::STAGE;
+        uint8_t* vs = ks + SM::BLK;
+        if (kb < n_cached && p.window <= 0) {
+          const int page = __shfl_sync(0xffffffffu, my_page, kb & 31);
+          if (page >= 0 && page < p.pages) {
+            if (lane == 0) {
+              const int64_t off = (((int64_t)p.full_layer * p.pages + page) * p.Hkv + g) * SM::BLK;
+              mbar_arrive_expect_tx(&full[st], 2 * SM::BLK);
+              bulk_load(ks, p.src_k8 + off, SM::BLK, &full[st]);
+              bulk_load(vs, p.src_v8 + off, SM::BLK, &full[st]);
+            }
+          } else {
+            // rows that stand for zero
+            if (lane == 0) record_error(p.err, HSWA_ERR_DEVICE_BOUNDS);
+            for (int r = lane; r < 64; r += 32) {
+              *i4_pair<D>(ks, 64, r) = 0u;
+              *i4_pair<D>(vs, 64, r) = 0u;
+            }
+            fence_proxy_async_smem();
+            if (lane == 0) mbar_arrive(&full[st]);
+          }
+          mbar_arrive(&full[st]);
+        } else if (kb < n_cached) {
+          const int pos0 = a + kb * 64;
+          const int nvalid = min(64, b - pos0);
+          if (ring_block >= 0) {
+            const uint8_t* rk = p.src_k8 + ring_block * p.blk_bytes;
+            const uint8_t* rv = p.src_v8 + ring_block * p.blk_bytes;
+            const int slot0 = pos0 % p.window;
+            auto wrap = [&](int r) {
+              int x = slot0 + r;
+              if (x >= p.window) x = p.window >= 64 ? x - p.window : x % p.window;
+              return x;
+            };
+            constexpr int CPR = D / 32;  // 16-byte chunks per row
+#pragma unroll 4
+            for (int i = lane; i < nvalid * CPR; i += 32) {
+              const int r = i / CPR, ch = i % CPR;
+              const int64_t off = (int64_t)wrap(r) * (D / 2) + ch * 16;
+              cp_async_16(smem_u32(ks) + i * 16, rk + off, 16);
+              cp_async_16(smem_u32(vs) + i * 16, rv + off, 16);
+            }
+            const int64_t pair0 = (int64_t)p.window * (D / 2);
+            for (int r = lane; r < nvalid; r += 32) {
+              const int64_t off = pair0 + (int64_t)wrap(r) * 4;
+              cp_async_4(smem_u32(i4_pair<D>(ks, 64, r)), rk + off);
+              cp_async_4(smem_u32(i4_pair<D>(vs, 64, r)), rv + off);
+            }
+          } else {
+            for (int r = lane; r < 64; r += 32) {
+              *i4_pair<D>(ks, 64, r) = 0u;
+              *i4_pair<D>(vs, 64, r) = 0u;
+            }
+          }
+          fence_proxy_async_smem();
+          if (lane == 0) mbar_arrive(&full[st]);
+          cp_async_arrive(&full[st]);
+        } else {
+          // the new tokens, as the cache will hold them: D / 8 lanes per row
+          constexpr int LPR = D / 8;
+          constexpr int RPP = 32 / LPR;  // rows per pass
+          const unsigned group = ((1u << LPR) - 1u) << (lane & ~(LPR - 1));
+          const int ch = lane % LPR;
+          for (int r0 = 0; r0 < p.n_qt; r0 += RPP) {
+            const int r = r0 + lane / LPR;
+            const bool live = r < p.n_qt;
+            const int64_t row = ((int64_t)s * p.n_qt + (live ? r : 0)) * p.Hkv + g;
+            const uint4 xk = __ldg(reinterpret_cast<const uint4*>(p.k_new + row * D) + ch);
+            const uint4 xv = __ldg(reinterpret_cast<const uint4*>(p.v_new + row * D) + ch);
+            const uint32_t wk[4] = {xk.x, xk.y, xk.z, xk.w}, wv[4] = {xv.x, xv.y, xv.z, xv.w};
+            RowRange ak, av;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              ak.add(wk[i]);
+              av.add(wv[i]);
+            }
+            ak.reduce<LPR>(group);
+            av.reduce<LPR>(group);
+            float ik, iv;
+            const uint32_t pk = i4_params(ak.lo, ak.hi, ak.finite, ik), pv2 = i4_params(av.lo, av.hi, av.finite, iv);
+            if (live) {
+              reinterpret_cast<uint32_t*>(i4_codes<D>(ks, r))[ch] = i4_pack8(wk, ak.lo, ik);
+              reinterpret_cast<uint32_t*>(i4_codes<D>(vs, r))[ch] = i4_pack8(wv, av.lo, iv);
+              if (ch == 0) {
+                *i4_pair<D>(ks, 64, r) = pk;
+                *i4_pair<D>(vs, 64, r) = pv2;
+              }
+            }
+          }
+          fence_proxy_async_smem();
+          if (lane == 0) mbar_arrive(&full[st]);
+          mbar_arrive(&full[st]);
+        }
+      }
+      if (!ok) break;
+    }
+    if (!ok) {
+      // copies in flight must land before the CTA may end (bounded; the error word is already set)
+      const uint32_t first = cnt > (uint32_t)NS ? cnt - NS : 0;
+      for (uint32_t x = first; x < cnt; ++x) (void)mbar_wait_limit(&full[x % NS], (x / NS) & 1, nullptr, kWaitLimitNs);
+      for (int x = it > 1 ? it - 1 : 0; x <= it; ++x)
+        (void)mbar_wait_limit(&item_full[x & 1], (x >> 1) & 1, nullptr, 10000000ull);
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  const int g8 = lane >> 2, t4 = lane & 3;
+  const int rg = RG == 2 ? warp & 1 : 0;
+  const int kw = RG == 2 ? warp >> 1 : warp;
+  const int row0 = rg * 8 * NT;
+  const int pi0 = (g8 >> 1) + 4 * (g8 & 1);  // key of S^T row g8 within a 16-key group (row g8 + 8: + 8)
+  float* m_w = reinterpret_cast<float*>(smem + SM::ML_OFF);  // [KW][ROWS]
+  float* l_w = m_w + I4_WARPS * ROWS;
+  float* b_w = l_w + I4_WARPS * ROWS;
+  float* e_w = b_w + I4_WARPS * ROWS;  // [I4_WARPS]
+  float* m_all = e_w + I4_WARPS;
+  float* l_all = m_all + ROWS;
+  float* b_all = l_all + ROWS;
+  float* area = reinterpret_cast<float*>(smem + SM::AREA_OFF);  // [2][ROWS][AREA_STRIDE]
+  uint32_t cnt = 0, ncons = 0;
+  auto cons_sync = [&]() -> bool {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(cons);
+    return warp_wait(cons, (ncons++) & 1, p.err);
+  };
+
+  for (int it = 0;; ++it) {
+    const int slot = it & 1;
+    if (!warp_wait(&item_full[slot], (it >> 1) & 1, p.err)) return;
+    const I4Item& I = items[slot];
+    if (I.item < 0) return;
+    const int L = I.L, ia = I.a, ib = I.b, n_cached = I.n_cached, n_blk = I.n_blk;
+
+    // ---- Q fragments: lane (g8, t4) holds dims [t4 D/4, +D/4) of row g8 of each n-tile
+    uint32_t qf[NT][NW][4];
+    float c1[NT][2], c2[NT][2];
+    int r_lo[NT][2], r_hi[NT][2];
+    float slope[NT][2];
+    int r_pos[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = row0 + nt * 8 + g8;
+      const bool live = r < p.R;
+      const uint4* src = reinterpret_cast<const uint4*>(smem + SM::Q_OFF + slot * SM::Q_BYTES + r * (D * 2)) +
+                         t4 * (D / 32);
+      uint32_t w[4 * NW];
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        const uint4 x = live ? src[i] : make_uint4(0, 0, 0, 0);
+        w[4 * i] = x.x;
+        w[4 * i + 1] = x.y;
+        w[4 * i + 2] = x.z;
+        w[4 * i + 3] = x.w;
+      }
+      float mx = 0.f, sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4 * NW; ++i) {
+        const float x0 = __uint_as_float(w[i] << 16), x1 = __uint_as_float(w[i] & 0xFFFF0000u);
+        mx = fmaxf(mx, fmaxf(fabsf(x0), fabsf(x1)));
+        sum += x0 + x1;
+      }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      int e = (__float_as_int(mx) >> 23) - 127;
+      e = e < -110 ? -110 : (e > 115 ? 115 : e);
+      const float f_lo = pow2i(14 - e), f_hi = f_lo * 0.0625f;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        // dims 8i .. 8i + 7: w[4i + j] holds dims 2j, 2j + 1
+        auto lo = [&](int j) { return __uint_as_float(w[4 * i + j] << 16) * f_lo; };
+        auto hi = [&](int j) { return __uint_as_float(w[4 * i + j] & 0xFFFF0000u) * f_hi; };
+        qf[nt][i][0] = pack_f16x2(lo(0), lo(2));
+        qf[nt][i][1] = pack_f16x2(hi(0), hi(2));
+        qf[nt][i][2] = pack_f16x2(lo(1), lo(3));
+        qf[nt][i][3] = pack_f16x2(hi(1), hi(3));
+      }
+      // scores from the accumulator: acc * 2^(e - 14 + 24) * step + lo * sum(q), times the softmax scale
+      const float sc = MOD ? p.scale_nat : p.scale_log2;
+      const float a1 = sc * pow2i(e + 10), a2 = sc * sum;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        c1[nt][c] = __shfl_sync(0xffffffffu, a1, (2 * t4 + c) * 4);
+        c2[nt][c] = __shfl_sync(0xffffffffu, a2, (2 * t4 + c) * 4);
+        const int rr = row0 + nt * 8 + 2 * t4 + c;
+        const int tok = rr < p.R ? rr / p.G : 0;
+        r_lo[nt][c] = I.row_lo[tok];
+        r_hi[nt][c] = I.row_hi[tok];
+        if constexpr (MOD) {
+          r_pos[nt][c] = L + tok;
+          slope[nt][c] = p.slope && rr < p.R ? p.slope[I.g * p.G + rr % p.G] * 1.4426950408889634f : 0.f;
+        }
+      }
+    }
+
+    float o[MT][NT][4];
+    float m[NT][2], l[NT][2], bs[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        m[nt][c] = -INFINITY;
+        l[nt][c] = 0.f;
+        bs[nt][c] = 0.f;
+      }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
+    int e_cur = -120;        // V steps are used divided by 2^e_cur
+    float sv_lim = -1.f;     // a step above this moves e_cur
+
+    for (int kb = 0; kb < n_blk; ++kb, ++cnt) {
+      const int st = cnt % NS;
+      if (!warp_wait(&full[st], (cnt / NS) & 1, p.err)) return;
+      uint8_t* ks = smem + st * SM::STAGE;
+      uint8_t* vs = ks + SM::BLK;
+      const bool is_new = kb >= n_cached;
+      const int kbase = is_new ? L : ia + kb * 64;
+      const int kend = is_new ? L + p.n_qt : ib;  // no key at or past this
+      const bool edge = kbase + 64 > min(kend, I.hi_min) || kbase < I.lo_max;
+#pragma unroll
+      for (int kg = 0; kg < KG; ++kg) {
+        const int key0 = (kw * KG + kg) * 16;
+        const int kpos = kbase + key0;
+        if (edge && (kpos >= kend || kpos + 16 <= I.lo_min)) continue;  // nothing in this group
+        // ---- S^T = K Q^T
+        uint32_t wl[NW], wh[NW];
+        {
+          const uint8_t* a0 = i4_codes<D>(ks, key0 + pi0) + t4 * (D / 8);
+          if constexpr (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(a0), y = *reinterpret_cast<const uint4*>(a0 + 8 * (D / 2));
+            wl[0] = x.x; wl[1] = x.y; wl[2] = x.z; wl[3] = x.w;
+            wh[0] = y.x; wh[1] = y.y; wh[2] = y.z; wh[3] = y.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(a0), y = *reinterpret_cast<const uint2*>(a0 + 8 * (D / 2));
+            wl[0] = x.x; wl[1] = x.y;
+            wh[0] = y.x; wh[1] = y.y;
+          }
+        }
+        uint32_t kp[2] = {*i4_pair<D>(ks, 64, key0 + pi0), *i4_pair<D>(ks, 64, key0 + pi0 + 8)};
+        uint32_t vp[2] = {*i4_pair<D>(vs, 64, key0 + pi0), *i4_pair<D>(vs, 64, key0 + pi0 + 8)};
+        if (edge) {  // rows no query row sees may hold anything: they stand for zero
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int key = kpos + pi0 + 8 * k;
+            if (key >= kend || key < I.lo_min) kp[k] = vp[k] = 0u;
+          }
+        }
+        float acc[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+#pragma unroll
+        for (int i = 0; i < NW; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t x = wl[i] >> (8 * h), y = wh[i] >> (8 * h);
+            const uint32_t a0 = x & 0x000F000Fu, a1 = y & 0x000F000Fu, a2 = x & 0x00F000F0u, a3 = y & 0x00F000F0u;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_f16(acc[nt], a0, a1, a2, a3, qf[nt][i][2 * h], qf[nt][i][2 * h + 1]);
+          }
+        // ---- scores in the log2 domain, masks, softmax weights
+        const float ksf[2] = {__uint_as_float(kp[0] << 16), __uint_as_float(kp[1] << 16)};
+        const float klf[2] = {__uint_as_float(kp[0] & 0xFFFF0000u), __uint_as_float(kp[1] & 0xFFFF0000u)};
+        float vsf[2] = {__uint_as_float(vp[0] << 16), __uint_as_float(vp[1] << 16)};
+        const float vlf[2] = {__uint_as_float(vp[0] & 0xFFFF0000u), __uint_as_float(vp[1] & 0xFFFF0000u)};
+        bool move = vsf[0] > sv_lim || vsf[1] > sv_lim;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int k = x >> 1, c = x & 1;
+            float z = fmaf(acc[nt][x] * ksf[k], c1[nt][c], klf[k] * c2[nt][c]);
+            if constexpr (MOD) {
+              const int key = kpos + pi0 + 8 * k;
+              z = p.softcap > 0.f ? capped_log2(z, p.cap_in, p.cap_log2) : z * 1.4426950408889634f;
+              if (p.slope) z = fmaf(-slope[nt][c], (float)abs(r_pos[nt][c] - key), z);
+            }
+            if (edge) {
+              const int key = kpos + pi0 + 8 * k;
+              if (key < r_lo[nt][c] || key >= r_hi[nt][c] || key >= kend) z = -INFINITY;
+            }
+            acc[nt][x] = z;
+            move = move || z > m[nt][c] + 8.f;
+          }
+        if (__any_sync(0xffffffffu, move)) {
+          float smax = fmaxf(vsf[0], vsf[1]);
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, x));
+          float osc = 1.f;
+          if (smax > sv_lim) {  // the same in every lane
+            int e = (int)((__float_as_uint(smax) >> 23) & 255u) - 127 - 6;  // steps at most 2^7
+            e = e < -120 ? -120 : e;
+            if (e > e_cur) {
+              osc = e - e_cur > 126 ? 0.f : pow2i(e_cur - e);
+              e_cur = e;
+            }
+            sv_lim = e_cur >= 120 ? 3.4e38f : pow2i(e_cur + 7);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float mx = fmaxf(acc[nt][c], acc[nt][2 + c]);
+#pragma unroll
+              for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+              const float mn = fmaxf(m[nt][c], mx);
+              const float al = mn == -INFINITY ? 1.f : ex2_approx(m[nt][c] - mn);
+              m[nt][c] = mn;
+              l[nt][c] *= al;
+              bs[nt][c] *= al;
+              const float f = al * osc;
+#pragma unroll
+              for (int i = 0; i < MT; ++i) {
+                o[i][nt][c] *= f;
+                o[i][nt][2 + c] *= f;
+              }
+            }
+        }
+        const float fe = pow2i(-e_cur);
+        vsf[0] *= fe;
+        vsf[1] *= fe;
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float w[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int k = x >> 1, c = x & 1;
+            const float moff = m[nt][c] == -INFINITY ? 0.f : m[nt][c];
+            const float e = ex2_approx(acc[nt][x] - moff);
+            l[nt][c] += e;
+            bs[nt][c] = fmaf(e, vlf[k], bs[nt][c]);
+            w[x] = e * vsf[k];
+          }
+          pb[nt][0] = movmatrix_t(pack_f16x2(w[0], w[1]));
+          pb[nt][1] = movmatrix_t(pack_f16x2(w[2], w[3]));
+        }
+        // ---- O^T += V^T P^T: this lane's dims [g8 D/8, +D/8) of keys t4, 4 + t4, 8 + t4, 12 + t4
+        {
+          const uint8_t* v0 = i4_codes<D>(vs, key0 + t4) + g8 * (D / 16);
+          constexpr int VW = D / 64;  // words per key
+          uint32_t vw[4][VW];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint8_t* src = v0 + 4 * j * (D / 2);
+            if constexpr (VW == 2) {
+              const uint2 x = *reinterpret_cast<const uint2*>(src);
+              vw[j][0] = x.x;
+              vw[j][1] = x.y;
+            } else {
+              vw[j][0] = *reinterpret_cast<const uint32_t*>(src);
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < VW; ++h)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              // four dims (8h + 4q ..) of the key pairs (t4, 4 + t4) and (8 + t4, 12 + t4)
+              const uint32_t u0 = __byte_perm(vw[0][h], vw[1][h], q ? 0x7632u : 0x5410u);
+              const uint32_t u1 = __byte_perm(vw[2][h], vw[3][h], q ? 0x7632u : 0x5410u);
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const uint32_t x0 = u0 >> (8 * y), x1 = u1 >> (8 * y);
+                const uint32_t a0 = x0 & 0x000F000Fu, a1 = x0 & 0x00F000F0u;
+                const uint32_t a2 = x1 & 0x000F000Fu, a3 = x1 & 0x00F000F0u;
+                const int i = 4 * h + 2 * q + y;  // dims 2i (rows 0-7) and 2i + 1 (rows 8-15) of this lane's
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma_f16(o[i][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+              }
+            }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+    }
+
+    // ---- merge the warps' states
+    const int s = I.s, hg = I.g, nsp = I.nsp, item = I.item;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) {
+          l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], x);
+          bs[nt][c] += __shfl_xor_sync(0xffffffffu, bs[nt][c], x);
+        }
+    if (!cons_sync()) return;  // the previous item's output has been read
+    if (lane == 0) mbar_arrive(&item_empty[slot]);
+    if (g8 == 0) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int r = row0 + nt * 8 + 2 * t4 + c;
+          m_w[kw * ROWS + r] = m[nt][c];
+          l_w[kw * ROWS + r] = l[nt][c];
+          b_w[kw * ROWS + r] = bs[nt][c];
+        }
+    }
+    if (!cons_sync()) return;
+    if (tid < ROWS) {
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < KW; ++w) M = fmaxf(M, m_w[w * ROWS + tid]);
+      const float Mo = M == -INFINITY ? 0.f : M;
+      float ls = 0.f, bb = 0.f;
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        const float f = ex2_approx(m_w[w * ROWS + tid] - Mo);
+        ls += l_w[w * ROWS + tid] * f;
+        bb += b_w[w * ROWS + tid] * f;
+      }
+      m_all[tid] = M;
+      l_all[tid] = ls;
+      b_all[tid] = bb;
+    }
+    {
+      float f[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int r = row0 + nt * 8 + 2 * t4 + c;
+          float M = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < KW; ++w) M = fmaxf(M, m_w[w * ROWS + r]);
+          f[nt][c] = M == -INFINITY ? 0.f : ex2_approx(m[nt][c] - M) * pow2i(e_cur);
+        }
+      // O^T accumulators: dims 2i hold 2^-24, dims 2i + 1 hold 2^-20 of the sum
+      auto put = [&](bool add) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int r = row0 + nt * 8 + 2 * t4 + c;
+            float* dst = area + ((kw & 1) * ROWS + r) * SM::AREA_STRIDE + g8 * (D / 8);
+#pragma unroll
+            for (int i = 0; i < MT; i += 2) {
+              float4 y = make_float4(o[i][nt][c] * f[nt][c] * 16777216.f, o[i][nt][2 + c] * f[nt][c] * 1048576.f,
+                                     o[i + 1][nt][c] * f[nt][c] * 16777216.f,
+                                     o[i + 1][nt][2 + c] * f[nt][c] * 1048576.f);
+              float4* d4 = reinterpret_cast<float4*>(dst + 2 * i);
+              if (add) {
+                const float4 z = *d4;
+                y.x += z.x; y.y += z.y; y.z += z.z; y.w += z.w;
+              }
+              *d4 = y;
+            }
+          }
+      };
+      if (kw < 2) put(false);
+      if (!cons_sync()) return;
+      if constexpr (KW == 4) {
+        if (kw >= 2) put(true);
+        if (!cons_sync()) return;
+      }
+    }
+    // ---- output: bf16 rows when the sequence has one split, else this item's partial
+    auto merged4 = [&](int r, int c) -> float4 {
+      const float4 x = *reinterpret_cast<const float4*>(area + r * SM::AREA_STRIDE + c);
+      const float4 y = *reinterpret_cast<const float4*>(area + (ROWS + r) * SM::AREA_STRIDE + c);
+      const float bb = b_all[r];
+      return make_float4(x.x + y.x + bb, x.y + y.y + bb, x.z + y.z + bb, x.w + y.w + bb);
+    };
+    float* part = reinterpret_cast<float*>(p.ws + p.part_off + (size_t)item * p.part_bytes);
+    for (int idx = tid; idx < p.R * (D / 4); idx += I4_WARPS * 32) {
+      const int r = idx / (D / 4), c = (idx % (D / 4)) * 4;
+      float4 x = merged4(r, c);
+      if (nsp == 1) {
+        const float ls = l_all[r];
+        const float inv = 1.f / ls;
+        if (ls == 0.f) x = make_float4(0.f, 0.f, 0.f, 0.f);  // a row that sees nothing
+        else x = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+        const int t = r / p.G, hh = r % p.G;
+        uint2 pk;
+        pk.x = pack_bf16x2(x.x, x.y);
+        pk.y = pack_bf16x2(x.z, x.w);
+        *reinterpret_cast<uint2*>(p.o + (((int64_t)s * p.n_qt + t) * p.Hq + hg * p.G + hh) * D + c) = pk;
+      } else {
+        *reinterpret_cast<float4*>(part + r * D + c) = x;
+      }
+    }
+    if (nsp > 1) {
+      for (int r = tid; r < p.R; r += I4_WARPS * 32) {
+        part[p.R * D + r] = m_all[r];
+        part[p.R * D + p.R + r] = l_all[r];
+      }
+    }
+  }
+}

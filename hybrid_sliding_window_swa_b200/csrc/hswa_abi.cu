@@ -13,6 +13,7 @@
 #include <vector>
 
 #include "internal.h"
+#include "kv_quant.cuh"
 
 namespace hswa {
 
@@ -106,8 +107,8 @@ static int check_desc(const hswa_pool_desc* d) {
     set_error("invalid pool descriptor (negative count or zero KV heads)");
     return HSWA_ERR_INVALID_ARG;
   }
-  if (d->kv_format != HSWA_KV_BF16 && d->kv_format != HSWA_KV_FP8_E4M3) {
-    set_error("kv_format %d unknown (HSWA_KV_BF16 or HSWA_KV_FP8_E4M3)", d->kv_format);
+  if (d->kv_format != HSWA_KV_BF16 && d->kv_format != HSWA_KV_FP8_E4M3 && d->kv_format != HSWA_KV_INT4) {
+    set_error("kv_format %d unknown (HSWA_KV_BF16, HSWA_KV_FP8_E4M3 or HSWA_KV_INT4)", d->kv_format);
     return HSWA_ERR_INVALID_ARG;
   }
   if (d->window < 1) {
@@ -142,6 +143,12 @@ static size_t scale_bytes(const hswa_pool_desc* d) {
   return round256(4 * sizeof(float) * (size_t)(d->n_swa_layers + d->n_full_layers) * d->n_kv_heads);
 }
 
+// Bytes of one block of `rows` rows (a ring row's W slots or a page's 64), K or V, one KV head.
+static int64_t block_bytes(const hswa_pool_desc* d, int64_t rows) {
+  if (d->kv_format == HSWA_KV_INT4) return i4_block_bytes(rows, d->head_dim);
+  return rows * d->head_dim * (d->kv_format == HSWA_KV_FP8_E4M3 ? 1 : 2);
+}
+
 }  // namespace hswa
 
 using namespace hswa;
@@ -153,12 +160,10 @@ const char* hswa_last_error(void) { return g_err; }
 int kv_pool_layout(const hswa_pool_desc* desc, size_t* bytes_total, size_t* bytes_swa, size_t* bytes_full) {
   int rc = check_desc(desc);
   if (rc) return rc;
-  const bool fp8 = desc->kv_format == HSWA_KV_FP8_E4M3;
-  const size_t e = fp8 ? 1 : 2;
   const size_t swa = round256(2 * (size_t)desc->max_seqs * desc->n_swa_layers * desc->n_kv_heads *
-                              (size_t)desc->window * desc->head_dim * e);
+                              (size_t)block_bytes(desc, desc->window));
   const size_t full = round256(2 * (size_t)desc->n_full_layers * (size_t)desc->pages_per_full_layer *
-                               desc->n_kv_heads * (size_t)desc->page_size * desc->head_dim * e);
+                               desc->n_kv_heads * (size_t)block_bytes(desc, desc->page_size));
   const size_t sc = scale_bytes(desc);
   if (bytes_swa) *bytes_swa = swa;
   if (bytes_full) *bytes_full = full;
@@ -204,11 +209,13 @@ int kv_pool_create(const hswa_pool_desc* desc, void* dev_mem, size_t bytes, hswa
   p->bytes_full = full;
   p->bytes_scales = sc_bytes;
   p->fp8 = desc->kv_format == HSWA_KV_FP8_E4M3;
+  p->i4 = desc->kv_format == HSWA_KV_INT4;
   p->esize = p->fp8 ? 1 : 2;
-  const size_t ring_half = (size_t)desc->max_seqs * desc->n_swa_layers * desc->n_kv_heads * (size_t)desc->window *
-                           desc->head_dim * p->esize;  // bytes
-  const size_t page_half = (size_t)desc->n_full_layers * (size_t)desc->pages_per_full_layer * desc->n_kv_heads *
-                           (size_t)desc->page_size * desc->head_dim * p->esize;
+  p->ring_blk = block_bytes(desc, desc->window);
+  p->page_blk = block_bytes(desc, desc->page_size);
+  const size_t ring_half = (size_t)desc->max_seqs * desc->n_swa_layers * desc->n_kv_heads * (size_t)p->ring_blk;
+  const size_t page_half =
+      (size_t)desc->n_full_layers * (size_t)desc->pages_per_full_layer * desc->n_kv_heads * (size_t)p->page_blk;
   p->ring_k8 = p->base;
   p->ring_v8 = p->base + ring_half;
   p->page_k8 = p->base + swa;
@@ -222,7 +229,7 @@ int kv_pool_create(const hswa_pool_desc* desc, void* dev_mem, size_t bytes, hswa
   const uint64_t D = desc->head_dim;
   p->ring_tma = false;
   const uint64_t ring_rows = (uint64_t)desc->max_seqs * desc->n_swa_layers * desc->n_kv_heads;
-  if (!p->fp8 && desc->window % 128 == 0 && ring_rows > 0) {
+  if (!p->fp8 && !p->i4 && desc->window % 128 == 0 && ring_rows > 0) {
     const uint64_t dims[3] = {D, (uint64_t)desc->window, ring_rows};
     const uint64_t strides[2] = {D * 2, (uint64_t)desc->window * D * 2};
     const uint32_t box[3] = {64, 128, 1};
@@ -240,7 +247,7 @@ int kv_pool_create(const hswa_pool_desc* desc, void* dev_mem, size_t bytes, hswa
     delete p;
     return HSWA_ERR_UNSUPPORTED_SHAPE;
   }
-  if (!p->fp8 && page_rows > 0) {
+  if (!p->fp8 && !p->i4 && page_rows > 0) {
     const uint64_t dims[3] = {D, (uint64_t)desc->page_size, page_rows};
     const uint64_t strides[2] = {D * 2, (uint64_t)desc->page_size * D * 2};
     const uint32_t box[3] = {64, 64, 1};
@@ -369,6 +376,126 @@ int kv_pool_gather_ring(hswa_pool* pool, int layer, int32_t dst_seq, const int32
   return launch_gather_ring(pool, layer, dst_seq, src_seq, static_cast<cudaStream_t>(stream));
 }
 
+static int check_rope(const hswa_rope_desc* r, int head_dim, const char* who) {
+  if (!r) {
+    set_error("%s: null rope descriptor", who);
+    return HSWA_ERR_INVALID_ARG;
+  }
+  if (r->rot_dim < 16 || r->rot_dim % 16 != 0 || r->rot_dim > head_dim) {
+    set_error("%s: rot_dim %d must be a multiple of 16 in 16 .. head_dim %d", who, r->rot_dim, head_dim);
+    return HSWA_ERR_UNSUPPORTED_SHAPE;
+  }
+  if (r->n_axes < 1 || r->n_axes > 4) {
+    set_error("%s: n_axes %d outside 1 .. 4", who, r->n_axes);
+    return HSWA_ERR_UNSUPPORTED_SHAPE;
+  }
+  for (int i = 0; i < r->rot_dim / 2; ++i)
+    if (r->axis[i] >= r->n_axes || !isfinite(r->inv_freq[i])) {
+      set_error("%s: pair %d has axis %d of %d or a frequency that is not finite", who, i, (int)r->axis[i], r->n_axes);
+      return HSWA_ERR_INVALID_ARG;
+    }
+  return HSWA_OK;
+}
+
+static int current_sms(const char* who, int* sms) {
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) {
+    set_error("%s: no current CUDA device: %s", who, cudaGetErrorString(e));
+    return HSWA_ERR_CUDA;
+  }
+  return HSWA_OK;
+}
+
+int rope_fwd(const hswa_rope_desc* rope, int head_dim, int64_t n_tokens, const int64_t* pos, const hswa_bf16* q,
+             hswa_bf16* q_out, int n_q_heads, const hswa_bf16* k, hswa_bf16* k_out, int n_kv_heads, void* stream) {
+  if (head_dim != 64 && head_dim != 128) {
+    set_error("rope_fwd: head_dim %d unsupported (64 or 128)", head_dim);
+    return HSWA_ERR_UNSUPPORTED_SHAPE;
+  }
+  int rc = check_rope(rope, head_dim, "rope_fwd");
+  if (rc) return rc;
+  if (n_tokens < 0 || n_q_heads < 0 || n_kv_heads < 0) {
+    set_error("rope_fwd: negative sizes");
+    return HSWA_ERR_INVALID_ARG;
+  }
+  if (n_q_heads > 65535 || n_kv_heads > 65535) {
+    set_error("rope_fwd: at most 65535 heads");
+    return HSWA_ERR_UNSUPPORTED_SHAPE;
+  }
+  if (n_tokens == 0 || n_q_heads + n_kv_heads == 0) return HSWA_OK;
+  if (!pos || (n_q_heads > 0 && (!q || !q_out || !aligned16(q) || !aligned16(q_out))) ||
+      (n_kv_heads > 0 && (!k || !k_out || !aligned16(k) || !aligned16(k_out)))) {
+    set_error("rope_fwd: missing or misaligned device pointer");
+    return HSWA_ERR_INVALID_ARG;
+  }
+  RopeLaunch L{};
+  if ((rc = current_sms("rope_fwd", &L.sms))) return rc;
+  L.rope = rope;
+  L.d = head_dim;
+  L.n = n_tokens;
+  L.pos = pos;
+  L.Hq = n_q_heads;
+  L.Hkv = n_kv_heads;
+  L.q = q;
+  L.q_out = q_out;
+  L.k = k;
+  L.k_out = k_out;
+  return launch_rope(L, static_cast<cudaStream_t>(stream));
+}
+
+int kv_pool_append_rope(hswa_pool* pool, int layer, const hswa_rope_desc* rope, const int64_t* pos, int n_seqs,
+                        const int32_t* seq_ids, const int64_t* start_pos, int n_tok, const hswa_bf16* q,
+                        hswa_bf16* q_out, int n_q_heads, const hswa_bf16* k, hswa_bf16* k_out, const hswa_bf16* v,
+                        const int32_t* page_table, int pt_stride, void* stream) {
+  if (!pool) {
+    set_error("kv_pool_append_rope: null pool");
+    return HSWA_ERR_INVALID_ARG;
+  }
+  const hswa_pool_desc& D = pool->desc;
+  if (layer < 0 || layer >= D.n_swa_layers + D.n_full_layers) {
+    set_error("kv_pool_append_rope: layer %d out of range", layer);
+    return HSWA_ERR_INVALID_ARG;
+  }
+  int rc = check_rope(rope, D.head_dim, "kv_pool_append_rope");
+  if (rc) return rc;
+  if ((rc = check_heads(pool, n_q_heads))) return rc;
+  if (n_seqs < 0 || n_tok < 0) {
+    set_error("kv_pool_append_rope: negative sizes");
+    return HSWA_ERR_INVALID_ARG;
+  }
+  if ((rc = check_device(pool, "kv_pool_append_rope"))) return rc;
+  if (n_seqs == 0 || n_tok == 0) return HSWA_OK;
+  const bool is_swa = layer < D.n_swa_layers;
+  if (!pos || !q || !q_out || !k || !v || !start_pos || !aligned16(q) || !aligned16(q_out) || !aligned16(k) ||
+      !aligned16(k_out) || !aligned16(v) || (is_swa && !seq_ids) || (!is_swa && (!page_table || pt_stride < 1))) {
+    set_error("kv_pool_append_rope: missing or misaligned device pointer");
+    return HSWA_ERR_INVALID_ARG;
+  }
+  RopeLaunch L{};
+  L.rope = rope;
+  L.d = D.head_dim;
+  L.sms = pool->sms;
+  L.n = (int64_t)n_seqs * n_tok;
+  L.pos = pos;
+  L.Hq = n_q_heads;
+  L.Hkv = D.n_kv_heads;
+  L.q = q;
+  L.q_out = q_out;
+  L.k = k;
+  L.k_out = k_out;
+  L.pool = pool;
+  L.layer = layer;
+  L.n_tok = n_tok;
+  L.v = v;
+  L.seq_ids = seq_ids;
+  L.start_pos = start_pos;
+  L.page_table = page_table;
+  L.pt_stride = pt_stride;
+  return launch_rope(L, static_cast<cudaStream_t>(stream));
+}
+
 static int build_q_map(CUtensorMap* m, const void* base, int B, int n_q, int H, int d) {
   const uint64_t dims[4] = {(uint64_t)d, (uint64_t)H, (uint64_t)n_q, (uint64_t)B};
   const uint64_t strides[3] = {(uint64_t)d * 2, (uint64_t)H * d * 2, (uint64_t)n_q * H * d * 2};
@@ -411,6 +538,10 @@ int swa_prefill_fwd(hswa_pool* pool, int layer, const hswa_bf16* q, const hswa_b
   if (start_pos && !seq_ids) {
     set_error("swa_prefill_fwd: seq_ids are required with start_pos");
     return HSWA_ERR_INVALID_ARG;
+  }
+  if (pool->i4 && start_pos) {
+    set_error("swa_prefill_fwd: a prefix in a 4-bit ring is not read");
+    return HSWA_ERR_UNSUPPORTED_SHAPE;
   }
   if (D.window == 1)  // the window is the diagonal alone: o_i = v_i
     return launch_window1(pool, v, o, B, n_q, n_q_heads, D.n_kv_heads, D.head_dim, static_cast<cudaStream_t>(stream));
@@ -493,8 +624,15 @@ int hybrid_decode_workspace_size(const hswa_pool* pool, int n_seqs, int n_q_per_
   int rc = check_heads(pool, n_q_heads);
   if (rc) return rc;
   const hswa_pool_desc& D = pool->desc;
-  // sized for a full layer, the larger of the two layer kinds
-  *bytes = decode_workspace_bytes(n_seqs, n_q_per_seq, n_q_heads, D.n_kv_heads, D.head_dim, 0, max_ctx_len);
+  // sized for a full layer, the larger of the two layer kinds; 4-bit pools and modified scores may cut
+  // the keys into shorter splits, and so need more
+  *bytes = decode_workspace_bytes(n_seqs, n_q_per_seq, n_q_heads, D.n_kv_heads, D.head_dim, 0, max_ctx_len, false);
+  const size_t ext =
+      decode_workspace_bytes(n_seqs, n_q_per_seq, n_q_heads, D.n_kv_heads, D.head_dim, 0, max_ctx_len, true);
+  const size_t ext_ring = decode_workspace_bytes(n_seqs, n_q_per_seq, n_q_heads, D.n_kv_heads, D.head_dim, D.window,
+                                                 max_ctx_len, true);
+  if (ext > *bytes) *bytes = ext;
+  if (D.n_swa_layers > 0 && ext_ring > *bytes) *bytes = ext_ring;
   return HSWA_OK;
 }
 
@@ -505,7 +643,7 @@ namespace hswa {
 int prepare_decode(hswa_pool* pool, const char* who, int layer, const uint16_t* q, const uint16_t* k_new,
                    const uint16_t* v_new, uint16_t* o, int n_seqs, int n_q_per_seq, const int64_t* ctx_len,
                    int64_t max_ctx_len, const int32_t* seq_ids, const int32_t* page_table, int pt_stride,
-                   int n_q_heads, DecodeLaunch* L, size_t* need) {
+                   int n_q_heads, const hswa_score_mod* mod, DecodeLaunch* L, size_t* need) {
   if (!pool) {
     set_error("%s: null pool", who);
     return HSWA_ERR_INVALID_ARG;
@@ -541,13 +679,17 @@ int prepare_decode(hswa_pool* pool, const char* who, int layer, const uint16_t* 
     return HSWA_ERR_INVALID_ARG;
   }
   const int window = is_swa ? D.window : 0;
-  const size_t msm = decode_merge_smem_bytes(n_seqs, n_q_per_seq, n_q_heads, D.n_kv_heads, window, max_ctx_len);
+  const bool ext = pool->i4 || mod;
+  const size_t msm = decode_merge_smem_bytes(n_seqs, n_q_per_seq, n_q_heads, D.n_kv_heads, window, max_ctx_len, ext);
   if (msm > (size_t)pool->smem_optin) {
     set_error("%s: max_ctx_len %lld gives %zu bytes of split-merge shared memory; this device allows %d", who,
               (long long)max_ctx_len, msm, pool->smem_optin);
     return HSWA_ERR_UNSUPPORTED_SHAPE;
   }
-  *need = decode_workspace_bytes(n_seqs, n_q_per_seq, n_q_heads, D.n_kv_heads, D.head_dim, window, max_ctx_len);
+  *need = decode_workspace_bytes(n_seqs, n_q_per_seq, n_q_heads, D.n_kv_heads, D.head_dim, window, max_ctx_len,
+                                 ext);
+  L->mod = mod;
+  L->ext = ext;
   L->n_seqs = n_seqs;
   L->layer = layer;
   L->n_qt = n_q_per_seq;
@@ -581,10 +723,42 @@ int hybrid_decode_fwd(hswa_pool* pool, int layer, const hswa_bf16* q, const hswa
   DecodeLaunch L;
   size_t need = 0;
   int rc = prepare_decode(pool, "hybrid_decode_fwd", layer, q, k_new, v_new, o, n_seqs, n_q_per_seq, ctx_len,
-                          max_ctx_len, seq_ids, page_table, pt_stride, n_q_heads, &L, &need);
+                          max_ctx_len, seq_ids, page_table, pt_stride, n_q_heads, nullptr, &L, &need);
   if (rc || L.n_seqs == 0) return rc;
   if (ws_bytes < need || (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)))) {
     set_error("hybrid_decode_fwd: workspace of %zu bytes (256-aligned) needed, %zu given", need, ws_bytes);
+    return HSWA_ERR_INVALID_ARG;
+  }
+  L.workspace = workspace;
+  L.ws_bytes = ws_bytes;
+  return launch_decode(L, static_cast<cudaStream_t>(stream));
+}
+
+static int check_mod(const hswa_score_mod* mod, const char* who) {
+  if (!mod) {
+    set_error("%s: null score modifications", who);
+    return HSWA_ERR_INVALID_ARG;
+  }
+  if (!(mod->softcap >= 0.0f) || !isfinite(mod->softcap)) {
+    set_error("%s: softcap must be 0 or finite and > 0", who);
+    return HSWA_ERR_INVALID_ARG;
+  }
+  return HSWA_OK;
+}
+
+int hybrid_decode_mod_fwd(hswa_pool* pool, int layer, const hswa_bf16* q, const hswa_bf16* k_new,
+                          const hswa_bf16* v_new, hswa_bf16* o, int n_seqs, int n_q_per_seq, const int64_t* ctx_len,
+                          int64_t max_ctx_len, const int32_t* seq_ids, const int32_t* page_table, int pt_stride,
+                          int n_q_heads, const hswa_score_mod* mod, void* workspace, size_t ws_bytes, void* stream) {
+  int rc = check_mod(mod, "hybrid_decode_mod_fwd");
+  if (rc) return rc;
+  DecodeLaunch L;
+  size_t need = 0;
+  rc = prepare_decode(pool, "hybrid_decode_mod_fwd", layer, q, k_new, v_new, o, n_seqs, n_q_per_seq, ctx_len,
+                      max_ctx_len, seq_ids, page_table, pt_stride, n_q_heads, mod, &L, &need);
+  if (rc || L.n_seqs == 0) return rc;
+  if (ws_bytes < need || (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)))) {
+    set_error("hybrid_decode_mod_fwd: workspace of %zu bytes (256-aligned) needed, %zu given", need, ws_bytes);
     return HSWA_ERR_INVALID_ARG;
   }
   L.workspace = workspace;

@@ -3,6 +3,7 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include "../../include/hswa.h"
@@ -15,7 +16,10 @@ struct hswa_pool {
   uint8_t* base;
   size_t bytes_swa, bytes_full, bytes_scales;
   bool fp8;          // entries are FP8 E4M3 codes (1 byte) instead of bf16 (2 bytes)
-  int esize;         // bytes per element
+  bool i4;           // rows are 4-bit codes with a (step, minimum) pair, see kv_quant.cuh
+  int esize;         // bytes per element (bf16 and FP8 pools)
+  int64_t ring_blk;  // bytes of one (sequence, layer, KV head) ring block and of one (page, KV head)
+  int64_t page_blk;  // block, K or V
   // element arrays (uint16_t for bf16 pools; for FP8 pools the same addresses hold bytes, see *8)
   uint16_t* ring_k;  // [max_seqs][n_swa][Hkv][W][d]
   uint16_t* ring_v;
@@ -55,6 +59,31 @@ bool make_tmap_u8(CUtensorMap* map, const void* base, int rank, const uint64_t* 
 int launch_append(const hswa_pool* pool, int layer, int n_seqs, const int32_t* seq_ids,
                   const int64_t* start_pos, int n_tok, const uint16_t* k, const uint16_t* v,
                   const int32_t* page_table, int pt_stride, cudaStream_t stream);
+
+// The destination of a commit into `layer`, as the commit kernels take it.
+void fill_commit_dst(const hswa_pool* pool, int layer, int n_tok, const int32_t* seq_ids, const int64_t* start_pos,
+                     const int32_t* page_table, int pt_stride, struct CommitDst* out);
+
+struct RopeLaunch {
+  const hswa_rope_desc* rope;
+  int d, sms;
+  int64_t n;           // tokens
+  const int64_t* pos;  // [n_axes][n]
+  int Hq, Hkv;
+  const uint16_t* q;
+  uint16_t* q_out;
+  const uint16_t* k;
+  uint16_t* k_out;
+  // with a commit (pool not null)
+  const hswa_pool* pool;
+  int layer, n_tok;
+  const uint16_t* v;
+  const int32_t* seq_ids;
+  const int64_t* start_pos;
+  const int32_t* page_table;
+  int pt_stride;
+};
+int launch_rope(const RopeLaunch& L, cudaStream_t stream);
 
 int launch_gather_ring(const hswa_pool* pool, int layer, int dst, const int32_t* src, cudaStream_t stream);
 
@@ -105,13 +134,15 @@ struct DecodeLaunch {
   int pt_stride;
   const hswa_pool* pool;
   int ring_layer, full_layer;
+  const hswa_score_mod* mod;  // null: plain scores
+  bool ext;                   // 4-bit pool or score modifications: splits of ext_split keys
   void* workspace;
   size_t ws_bytes;
 };
 
-size_t decode_workspace_bytes(int n_seqs, int n_qt, int Hq, int Hkv, int d, int window, int64_t max_ctx_len);
+size_t decode_workspace_bytes(int n_seqs, int n_qt, int Hq, int Hkv, int d, int window, int64_t max_ctx_len, bool ext);
 // Dynamic shared memory of the split merge for these arguments (0 when no sequence can have two splits).
-size_t decode_merge_smem_bytes(int n_seqs, int n_qt, int Hq, int Hkv, int window, int64_t max_ctx_len);
+size_t decode_merge_smem_bytes(int n_seqs, int n_qt, int Hq, int Hkv, int window, int64_t max_ctx_len, bool ext);
 
 // Argument checks shared by hybrid_decode_fwd and hybrid_decode_fwd_noalloc (messages name `who`).
 // On HSWA_OK, *L is filled except for workspace/ws_bytes and *need is the scratch the call uses;
@@ -119,7 +150,7 @@ size_t decode_merge_smem_bytes(int n_seqs, int n_qt, int Hq, int Hkv, int window
 int prepare_decode(hswa_pool* pool, const char* who, int layer, const uint16_t* q, const uint16_t* k_new,
                    const uint16_t* v_new, uint16_t* o, int n_seqs, int n_q_per_seq, const int64_t* ctx_len,
                    int64_t max_ctx_len, const int32_t* seq_ids, const int32_t* page_table, int pt_stride,
-                   int n_q_heads, DecodeLaunch* L, size_t* need);
+                   int n_q_heads, const hswa_score_mod* mod, DecodeLaunch* L, size_t* need);
 int launch_decode(const DecodeLaunch& L, cudaStream_t stream);
 
 }  // namespace hswa

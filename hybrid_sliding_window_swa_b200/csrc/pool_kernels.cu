@@ -6,6 +6,8 @@
 // Window-safe length: "MiMo v2.5 inference optimisation", section "KV cache redesign".
 #include "common.cuh"
 #include "internal.h"
+#include "kv_place.cuh"
+#include "kv_quant.cuh"
 
 namespace hswa {
 
@@ -81,6 +83,76 @@ __global__ void __launch_bounds__(256) append_kernel(
   }
 }
 
+// Commit into a 4-bit pool: one thread reads 16 bytes (8 entries) of K and of V, the D / 8 threads of
+// a row find its range by shuffles, and each writes 4 bytes of codes (the first one the row's pair
+// too). Bound by HBM: 2 d bytes in and d / 2 + 4 out per row; K and V in one thread keep two loads in
+// flight through the shuffles.
+template <int D>
+__global__ void __launch_bounds__(256) append_i4_kernel(const uint16_t* __restrict__ k,
+                                                        const uint16_t* __restrict__ v, int64_t rows, CommitDst dst) {
+  constexpr int PER_ROW = D / 8;
+  const int64_t total = rows * PER_ROW;
+  const unsigned group = (PER_ROW == 16 ? 0xFFFFu : 0xFFu) << ((threadIdx.x & 31) & ~(PER_ROW - 1));
+  for (int64_t idx = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; idx < total;
+       idx += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t row = idx / PER_ROW;
+    const int c = (int)(idx % PER_ROW);
+    const int g = (int)(row % dst.Hkv);
+    const int64_t bt = row / dst.Hkv;
+    const int t = (int)(bt % dst.n_tok);
+    int64_t block, r;
+    // a row's threads leave together: the place depends on the row alone
+    if (!commit_place(dst, (int)(bt / dst.n_tok), t, g, block, r)) continue;
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(k + row * D) + c);
+    const uint4 b = __ldg(reinterpret_cast<const uint4*>(v + row * D) + c);
+    const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
+    RowRange ra, rb;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      ra.add(wa[i]);
+      rb.add(wb[i]);
+    }
+    ra.reduce<PER_ROW>(group);
+    rb.reduce<PER_ROW>(group);
+    float ia, ib;
+    const uint32_t pa = i4_params(ra.lo, ra.hi, ra.finite, ia), pb = i4_params(rb.lo, rb.hi, rb.finite, ib);
+    const int64_t n_rows = dst.is_swa ? dst.W : 64;
+    uint8_t* bk = dst.k + block * i4_block_bytes(n_rows, D);
+    uint8_t* bv = dst.v + block * i4_block_bytes(n_rows, D);
+    reinterpret_cast<uint32_t*>(i4_codes<D>(bk, r))[c] = i4_pack8(wa, ra.lo, ia);
+    reinterpret_cast<uint32_t*>(i4_codes<D>(bv, r))[c] = i4_pack8(wb, rb.lo, ib);
+    if (c == 0) {
+      *i4_pair<D>(bk, n_rows, r) = pa;
+      *i4_pair<D>(bv, n_rows, r) = pb;
+    }
+  }
+}
+
+void fill_commit_dst(const hswa_pool* pool, int layer, int n_tok, const int32_t* seq_ids, const int64_t* start_pos,
+                     const int32_t* page_table, int pt_stride, CommitDst* out) {
+  const hswa_pool_desc& D = pool->desc;
+  const bool is_swa = layer < D.n_swa_layers;
+  const int n_layers = D.n_swa_layers + D.n_full_layers;
+  *out = CommitDst{};
+  out->k = is_swa ? pool->ring_k8 : pool->page_k8;
+  out->v = is_swa ? pool->ring_v8 : pool->page_v8;
+  out->start_pos = start_pos;
+  out->seq_ids = seq_ids;
+  out->page_table = page_table;
+  out->pt_stride = pt_stride;
+  out->is_swa = is_swa;
+  out->W = D.window;
+  out->n_swa = D.n_swa_layers;
+  out->layer = is_swa ? layer : layer - D.n_swa_layers;
+  out->max_seqs = D.max_seqs;
+  out->Hkv = D.n_kv_heads;
+  out->n_tok = n_tok;
+  out->pages = D.pages_per_full_layer;
+  out->inv_k = pool->fp8 ? pool->scales + ((size_t)2 * n_layers + layer) * D.n_kv_heads : nullptr;
+  out->inv_v = pool->fp8 ? pool->scales + ((size_t)3 * n_layers + layer) * D.n_kv_heads : nullptr;
+  out->err = pool->err;
+}
+
 int launch_append(const hswa_pool* pool, int layer, int n_seqs, const int32_t* seq_ids,
                   const int64_t* start_pos, int n_tok, const uint16_t* k, const uint16_t* v,
                   const int32_t* page_table, int pt_stride, cudaStream_t stream) {
@@ -97,6 +169,19 @@ int launch_append(const hswa_pool* pool, int layer, int n_seqs, const int32_t* s
   const int n_layers = D.n_swa_layers + D.n_full_layers;
   const float* inv_k = pool->fp8 ? pool->scales + ((size_t)2 * n_layers + layer) * D.n_kv_heads : nullptr;
   const float* inv_v = pool->fp8 ? pool->scales + ((size_t)3 * n_layers + layer) * D.n_kv_heads : nullptr;
+  if (pool->i4) {
+    CommitDst dst;
+    fill_commit_dst(pool, layer, n_tok, seq_ids, start_pos, page_table, pt_stride, &dst);
+    const int64_t rows = (int64_t)n_seqs * n_tok * D.n_kv_heads;
+    if (D.head_dim == 128) append_i4_kernel<128><<<grid, 256, 0, stream>>>(k, v, rows, dst);
+    else append_i4_kernel<64><<<grid, 256, 0, stream>>>(k, v, rows, dst);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) {
+      set_error("kv_pool_append: launch failed: %s", cudaGetErrorString(e));
+      return HSWA_ERR_CUDA;
+    }
+    return HSWA_OK;
+  }
 #define HSWA_APPEND(DD, F8)                                                                                    \
   append_kernel<DD, F8><<<grid, 256, 0, stream>>>(k, v, n_seqs, n_tok, D.n_kv_heads, start_pos, seq_ids,     \
                                                    page_table, pt_stride, dk, dv, is_swa, D.window,          \
@@ -144,8 +229,58 @@ __global__ void __launch_bounds__(256) gather_ring_kernel(uint8_t* __restrict__ 
   }
 }
 
+// gather_ring_kernel for a 4-bit pool: one thread per (slot, KV head) and 16 bytes of codes, the first
+// one of a row also moves the row's pair.
+template <int D>
+__global__ void __launch_bounds__(256) gather_ring_i4_kernel(uint8_t* __restrict__ ring_k, uint8_t* __restrict__ ring_v,
+                                                             const int32_t* __restrict__ src, int W, int Hkv,
+                                                             int n_swa, int layer, int max_seqs, int dst, int* err) {
+  constexpr int PER_ROW = D / 32;
+  const int64_t total = (int64_t)W * Hkv * PER_ROW;
+  const int64_t blk = i4_block_bytes(W, D);
+  for (int64_t idx = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; idx < total;
+       idx += (int64_t)gridDim.x * blockDim.x) {
+    const int c = (int)(idx % PER_ROW);
+    const int64_t row = idx / PER_ROW;
+    const int g = (int)(row % Hkv);
+    const int slot = (int)(row / Hkv);
+    const int sq = src[slot];
+    if (sq < 0 || sq == dst) continue;
+    if (sq >= max_seqs) {
+      record_error(err, HSWA_ERR_DEVICE_BOUNDS);
+      continue;
+    }
+    const int64_t from = (((int64_t)sq * n_swa + layer) * Hkv + g) * blk;
+    const int64_t to = (((int64_t)dst * n_swa + layer) * Hkv + g) * blk;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      uint8_t* ring = kv ? ring_v : ring_k;
+      reinterpret_cast<uint4*>(i4_codes<D>(ring + to, slot))[c] =
+          reinterpret_cast<const uint4*>(i4_codes<D>(ring + from, slot))[c];
+      if (c == 0) *i4_pair<D>(ring + to, W, slot) = *i4_pair<D>(ring + from, W, slot);
+    }
+  }
+}
+
 int launch_gather_ring(const hswa_pool* pool, int layer, int dst, const int32_t* src, cudaStream_t stream) {
   const hswa_pool_desc& D = pool->desc;
+  if (pool->i4) {
+    const int64_t n = (int64_t)D.window * D.n_kv_heads * (D.head_dim / 32);
+    const int64_t want = (n + 255) / 256;
+    const int grid = (int)(want < (int64_t)pool->sms * 8 ? want : (int64_t)pool->sms * 8);
+    if (D.head_dim == 128)
+      gather_ring_i4_kernel<128><<<grid, 256, 0, stream>>>(pool->ring_k8, pool->ring_v8, src, D.window, D.n_kv_heads,
+                                                           D.n_swa_layers, layer, D.max_seqs, dst, pool->err);
+    else
+      gather_ring_i4_kernel<64><<<grid, 256, 0, stream>>>(pool->ring_k8, pool->ring_v8, src, D.window, D.n_kv_heads,
+                                                          D.n_swa_layers, layer, D.max_seqs, dst, pool->err);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) {
+      set_error("kv_pool_gather_ring: launch failed: %s", cudaGetErrorString(e));
+      return HSWA_ERR_CUDA;
+    }
+    return HSWA_OK;
+  }
   const int row_bytes = D.head_dim * pool->esize;  // 64, 128 or 256
   const int64_t total = (int64_t)D.window * D.n_kv_heads * (row_bytes / 16);
   const int64_t want = (total + 255) / 256;

@@ -62,6 +62,7 @@ extern "C" {
 /* Storage format of a pool's K/V entries (hswa_pool_desc.kv_format). */
 #define HSWA_KV_BF16 0     /* bf16, as given */
 #define HSWA_KV_FP8_E4M3 1 /* FP8 E4M3 codes with a scale per (layer, KV head) and K/V, see kv_pool_set_scales */
+#define HSWA_KV_INT4 2     /* 4-bit codes with a (step, minimum) pair per row (token, KV head, K or V) */
 
 typedef uint16_t hswa_bf16;
 typedef struct hswa_pool hswa_pool;
@@ -80,7 +81,7 @@ typedef struct hswa_pool_desc {
   int32_t head_dim;              /* 64 or 128 */
   int32_t page_size;             /* 64 */
   int32_t max_seqs;              /* number of ring rows (sequence ids 0 .. max_seqs-1) */
-  int32_t kv_format;             /* HSWA_KV_BF16 or HSWA_KV_FP8_E4M3 */
+  int32_t kv_format;             /* HSWA_KV_BF16, HSWA_KV_FP8_E4M3 or HSWA_KV_INT4 */
   int64_t pages_per_full_layer;  /* >= 0 */
 } hswa_pool_desc;
 
@@ -100,7 +101,18 @@ typedef struct hswa_pool_desc {
  * +-448; OCP 8-bit floating point E4M3) and stands for the value E4M3_value(code) * s, where s is
  * the scale of its layer, KV head and K or V ("MiMo v2.5 inference optimisation", closing
  * section: quantization cuts the bits per cached entry and stacks with the window's cut in
- * entries). Any output pointer may be NULL. */
+ * entries).
+ * A 4-bit pool (HSWA_KV_INT4) holds each row x[0..head_dim) (one token, one KV head, K or V) as
+ *   lo = min x, step = bf16((max x - lo) * fp32(1/15)), code = clamp(rint((x - lo) * fp32(1/step)), 0, 15)
+ * (fp32, one rounding per operation; codes 0 where step is 0) and it stands for fp32(code * step + lo).
+ * Steps below 2^-120 are held as 0. A row with a NaN or an infinity, or whose range passes the fp32
+ * range, stands for NaN throughout. Its regions are made of blocks, one per (ring row, KV head) with
+ * R = W rows and one per (page, KV head) with R = page_size rows:
+ *   [R][head_dim / 2] bytes, dim 2i in the low and dim 2i + 1 in the high nibble of byte i, then
+ *   [R] pairs of bf16 (step, lo), padded to 16 bytes
+ *   ring  K then V : [2][max_seqs][n_swa_layers][n_kv_heads] blocks
+ *   pages K then V : [2][n_full_layers][pages_per_full_layer][n_kv_heads] blocks
+ * (head_dim 128: 68 bytes per row against 256 in a bf16 pool). Any output pointer may be NULL. */
 HSWA_API int kv_pool_layout(const hswa_pool_desc* desc, size_t* bytes_total, size_t* bytes_swa,
                    size_t* bytes_full);
 
@@ -120,7 +132,7 @@ HSWA_API int kv_pool_set_scales(hswa_pool* pool, int layer, const float* k_scale
 /* Release the host-side handle (not the device memory). NULL is accepted. */
 HSWA_API int kv_pool_destroy(hswa_pool* pool);
 
-/* Commit n_tok new tokens per sequence into layer `layer` (quantized to FP8 in an FP8 pool).
+/* Commit n_tok new tokens per sequence into layer `layer` (quantized in an FP8 or a 4-bit pool).
  *  k, v       [n_seqs][n_tok][n_kv_heads][head_dim] bf16, token t of row b sits at
  *             absolute position start_pos[b] + t.
  *  start_pos  device int64[n_seqs], >= 0.
@@ -137,8 +149,46 @@ HSWA_API int kv_pool_append(hswa_pool* pool, int layer, int n_seqs, const int32_
                    const int64_t* start_pos, int n_tok, const hswa_bf16* k, const hswa_bf16* v,
                    const int32_t* page_table, int pt_stride, void* stream);
 
+/* Rotary positions over several axes. A token has one position per axis (text: one axis; images and
+ * video: time, height, width). Pair i of the first rot_dim entries of every head is turned by the
+ * angle theta_i = position[axis[i]] * inv_freq[i]:
+ *   (x, y) -> (x cos theta_i - y sin theta_i, y cos theta_i + x sin theta_i)
+ * where the pair is entries (i, i + rot_dim / 2), or (2i, 2i + 1) when `interleaved` is not 0; entries
+ * past rot_dim pass unchanged. Angles are formed in 64 bits, the turn in fp32, results rounded to bf16
+ * once. Host values, read at the call. Positions may be any integers of magnitude below 2^53. */
+typedef struct hswa_rope_desc {
+  int32_t rot_dim;     /* multiple of 16, 16 .. head_dim */
+  int32_t n_axes;      /* 1 .. 4 */
+  int32_t interleaved;
+  int32_t reserved;    /* 0 */
+  double inv_freq[64]; /* radians per position of pair i, finite; i < rot_dim / 2 */
+  uint8_t axis[64];    /* axis of pair i, < n_axes */
+} hswa_rope_desc;
+
+/* Rotate the queries and keys of n_tokens tokens.
+ *  pos       device int64[n_axes][n_tokens]
+ *  q, q_out  [n_tokens][n_q_heads][head_dim] bf16;  k, k_out [n_tokens][n_kv_heads][head_dim] bf16.
+ * q_out may be q and k_out may be k (in place); other overlaps are not allowed. n_q_heads or
+ * n_kv_heads may be 0 (its pointers are then not used). Runs on the current device. */
+HSWA_API int rope_fwd(const hswa_rope_desc* rope, int head_dim, int64_t n_tokens, const int64_t* pos,
+                      const hswa_bf16* q, hswa_bf16* q_out, int n_q_heads, const hswa_bf16* k, hswa_bf16* k_out,
+                      int n_kv_heads, void* stream);
+
+/* rope_fwd and kv_pool_append in one pass: rotate q and k of n_tok tokens per sequence and commit the
+ * rotated keys and the values into layer `layer` (the pool's head_dim and n_kv_heads). The pool ends
+ * up as after rope_fwd and kv_pool_append of its k_out and v.
+ *  pos as in rope_fwd with n_tokens = n_seqs * n_tok (token t of sequence b at b * n_tok + t): the
+ *  rotary positions; where the tokens are kept is given by start_pos, seq_ids and page_table as in
+ *  kv_pool_append. k_out may be NULL when the rotated keys are needed in the pool only. For a
+ *  sliding-window layer, whose prefill reads the ring as it was before the chunk, use rope_fwd, the
+ *  prefill and kv_pool_append instead, unless nothing of the old ring is needed. */
+HSWA_API int kv_pool_append_rope(hswa_pool* pool, int layer, const hswa_rope_desc* rope, const int64_t* pos, int n_seqs,
+                                 const int32_t* seq_ids, const int64_t* start_pos, int n_tok, const hswa_bf16* q,
+                                 hswa_bf16* q_out, int n_q_heads, const hswa_bf16* k, hswa_bf16* k_out,
+                                 const hswa_bf16* v, const int32_t* page_table, int pt_stride, void* stream);
+
 /* Assemble ring row dst_seq of sliding-window layer `layer` slot by slot (entries are copied as
- * stored, bf16 or FP8): for each slot s with
+ * stored, bf16, FP8 or 4-bit): for each slot s with
  * src_seq[s] >= 0, the K and V rows of slot s (all KV heads) are copied from ring row src_seq[s];
  * slots with src_seq[s] = -1 or src_seq[s] = dst_seq are left as they are. Since every ring keeps
  * position p in slot p mod W, this moves cached window positions held by other sequences' rings
@@ -205,6 +255,33 @@ HSWA_API int hybrid_decode_fwd(hswa_pool* pool, int layer, const hswa_bf16* q, c
                       const int64_t* ctx_len, int64_t max_ctx_len, const int32_t* seq_ids,
                       const int32_t* page_table, int pt_stride, int n_q_heads, void* workspace,
                       size_t ws_bytes, void* stream);
+
+/* Changes to the scores and the visible keys of an attention call. The score of the query at position
+ * i for the key at position j, s = q.k / sqrt(head_dim), becomes
+ *   z = cap(s) - dist_slope[h] * |i - j|,  cap(s) = softcap * tanh(s / softcap)
+ * for query head h, and the query sees the keys j with
+ *   key_begin <= j < key_end  (its own entries of the two arrays)
+ * instead of the causal 0 <= j <= i. Sliding-window layers also need i - W < j < i + W. Positions that
+ * do not exist are never seen: j < 0, and j at or past the end of the chunk (prefill: start_pos + n_q)
+ * or of the new tokens (decode: ctx_len + n_q_per_seq). So packed documents pass the first position of
+ * the query's document as key_begin; a prefix (or image) seen in both directions passes its end as
+ * key_end; a padded row passes key_end <= key_begin. A query that sees no key gives zeros.
+ * What a query does not see changes nothing in its row whatever its keys hold; its values must be
+ * finite (entries no query of the call sees may hold anything). */
+typedef struct hswa_score_mod {
+  float softcap;             /* 0: none; else finite and > 0 */
+  const float* dist_slope;   /* device float32[n_q_heads], finite; NULL: none */
+  const int64_t* key_begin;  /* device int64[B][n_q], any values; NULL: 0 */
+  const int64_t* key_end;    /* device int64[B][n_q], any values; NULL: i + 1 */
+} hswa_score_mod;
+
+/* hybrid_decode_fwd with modified scores. key_begin and key_end are [n_seqs][n_q_per_seq]. Same
+ * workspace (hybrid_decode_workspace_size) and supported pools. */
+HSWA_API int hybrid_decode_mod_fwd(hswa_pool* pool, int layer, const hswa_bf16* q, const hswa_bf16* k_new,
+                                   const hswa_bf16* v_new, hswa_bf16* o, int n_seqs, int n_q_per_seq,
+                                   const int64_t* ctx_len, int64_t max_ctx_len, const int32_t* seq_ids,
+                                   const int32_t* page_table, int pt_stride, int n_q_heads,
+                                   const hswa_score_mod* mod, void* workspace, size_t ws_bytes, void* stream);
 
 /* Largest scratch hybrid_decode_fwd_noalloc can use: 64 MiB. */
 #define HSWA_NOALLOC_SCRATCH_BYTES (64u * 1024u * 1024u)
