@@ -37,6 +37,7 @@ EXPORTED = [
     "hswa_tree_release", "hswa_tree_evict_swa", "hswa_tree_match", "hswa_tree_match_batch", "hswa_tree_stats",
     "hswa_tree_match_slots", "kv_pool_gather_ring", "kv_pool_set_scales", "hswa_shard_kv_heads",
     "hswa_shard_sequences", "rope_fwd", "kv_pool_append_rope", "hybrid_decode_mod_fwd",
+    "prefill_mod_workspace_size", "swa_prefill_mod_fwd", "full_prefill_mod_fwd",
 ]
 
 # scratch bytes available to hybrid_decode_fwd_noalloc (HSWA_NOALLOC_SCRATCH_BYTES in hswa.h)
@@ -108,6 +109,9 @@ def load_library(path: str | None = None):
         "kv_pool_append_rope": [p, i32, ctypes.POINTER(RopeDescC), p, i32, p, p, i32, p, p, i32, p, p, p, p, i32, p],
         "hybrid_decode_mod_fwd": [p, i32, p, p, p, p, i32, i32, p, i64, p, p, i32, i32, ctypes.POINTER(ScoreModC), p,
                                   sz, p],
+        "prefill_mod_workspace_size": [p, i32, i32, ctypes.POINTER(sz)],
+        "swa_prefill_mod_fwd": [p, i32, p, p, p, p, i32, i32, p, p, i32, ctypes.POINTER(ScoreModC), p, sz, p],
+        "full_prefill_mod_fwd": [p, i32, p, p, i32, i32, p, p, i32, i32, ctypes.POINTER(ScoreModC), p, sz, p],
         "hswa_tree_evict_swa": [p, p, i64, i64, i64, ctypes.POINTER(i64)],
         "hswa_tree_match": [p, p, i64, ctypes.POINTER(i64), ctypes.POINTER(i64)],
         "hswa_tree_match_batch": [p, p, p, ctypes.c_int32, p, p],
@@ -405,6 +409,47 @@ def full_prefill_fwd(pool: KVPool, layer: int, q: torch.Tensor, page_table: torc
         pool.handle, layer, _ptr(q, torch.bfloat16, "q"), _ptr(o, torch.bfloat16, "o"), B, n_q,
         _ptr(start_pos, torch.int64, "start_pos"), _ptr(page_table, torch.int32, "page_table"),
         page_table.shape[1], hq, _stream(stream)))
+    return o
+
+
+def prefill_mod_workspace_size(pool: KVPool, B: int, n_q: int) -> int:
+    """Workspace bytes of a prefill with key ranges."""
+    out = ctypes.c_size_t()
+    _check(load_library().prefill_mod_workspace_size(pool.handle, B, n_q, ctypes.byref(out)))
+    return out.value
+
+
+def swa_prefill_mod_fwd(pool: KVPool, layer: int, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, mod: ScoreMod,
+                        workspace: torch.Tensor | None = None, o: torch.Tensor | None = None,
+                        start_pos: torch.Tensor | None = None, seq_ids: torch.Tensor | None = None,
+                        stream=None) -> torch.Tensor:
+    """swa_prefill_fwd with modified scores (key ranges [B, n_q] need the workspace)."""
+    B, n_q, hq, _ = q.shape
+    if o is None:
+        o = torch.empty_like(q)
+    m = mod.c((B, n_q), hq)
+    _check(load_library().swa_prefill_mod_fwd(
+        pool.handle, layer, _ptr(q, torch.bfloat16, "q"), _ptr(k, torch.bfloat16, "k"),
+        _ptr(v, torch.bfloat16, "v"), _ptr(o, torch.bfloat16, "o"), B, n_q,
+        _ptr(start_pos, torch.int64, "start_pos"), _ptr(seq_ids, torch.int32, "seq_ids"), hq, ctypes.byref(m),
+        _ptr(workspace, torch.uint8, "workspace"), workspace.numel() if workspace is not None else 0,
+        _stream(stream)))
+    return o
+
+
+def full_prefill_mod_fwd(pool: KVPool, layer: int, q: torch.Tensor, page_table: torch.Tensor, mod: ScoreMod,
+                         workspace: torch.Tensor | None = None, o: torch.Tensor | None = None,
+                         start_pos: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """full_prefill_fwd with modified scores (key ranges [B, n_q] need the workspace)."""
+    B, n_q, hq, _ = q.shape
+    if o is None:
+        o = torch.empty_like(q)
+    m = mod.c((B, n_q), hq)
+    _check(load_library().full_prefill_mod_fwd(
+        pool.handle, layer, _ptr(q, torch.bfloat16, "q"), _ptr(o, torch.bfloat16, "o"), B, n_q,
+        _ptr(start_pos, torch.int64, "start_pos"), _ptr(page_table, torch.int32, "page_table"),
+        page_table.shape[1], hq, ctypes.byref(m), _ptr(workspace, torch.uint8, "workspace"),
+        workspace.numel() if workspace is not None else 0, _stream(stream)))
     return o
 
 

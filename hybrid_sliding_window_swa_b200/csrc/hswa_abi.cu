@@ -511,39 +511,61 @@ static int build_o_map(CUtensorMap* m, void* base, int B, int n_q, int H, int d)
   return make_tmap_bf16(m, base, 4, dims, strides, box) ? HSWA_OK : HSWA_ERR_CUDA;
 }
 
-int swa_prefill_fwd(hswa_pool* pool, int layer, const hswa_bf16* q, const hswa_bf16* k, const hswa_bf16* v,
-                    hswa_bf16* o, int B, int n_q, const int64_t* start_pos, const int32_t* seq_ids, int n_q_heads,
-                    void* stream) {
+static int check_mod(const hswa_score_mod* mod, const char* who) {
+  if (!mod) {
+    set_error("%s: null score modifications", who);
+    return HSWA_ERR_INVALID_ARG;
+  }
+  if (!(mod->softcap >= 0.0f) || !isfinite(mod->softcap)) {
+    set_error("%s: softcap must be 0 or finite and > 0", who);
+    return HSWA_ERR_INVALID_ARG;
+  }
+  return HSWA_OK;
+}
+
+// Key ranges of a prefill need a workspace.
+static int check_mod_workspace(const hswa_score_mod* mod, int B, int n_q, const void* ws, size_t ws_bytes,
+                               const char* who) {
+  if (!mod->key_begin && !mod->key_end) return HSWA_OK;
+  const size_t need = prefill_mod_bytes(B, n_q);
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < need) {
+    set_error("%s: workspace of %zu bytes (256-aligned) needed with key ranges, %zu given", who, need, ws_bytes);
+    return HSWA_ERR_INVALID_ARG;
+  }
+  return HSWA_OK;
+}
+
+static int swa_prefill(const char* who, hswa_pool* pool, int layer, const hswa_bf16* q, const hswa_bf16* k,
+                       const hswa_bf16* v, hswa_bf16* o, int B, int n_q, const int64_t* start_pos,
+                       const int32_t* seq_ids, int n_q_heads, const hswa_score_mod* mod, void* workspace,
+                       size_t ws_bytes, void* stream) {
   if (!pool) {
-    set_error("swa_prefill_fwd: null pool");
+    set_error("%s: null pool", who);
     return HSWA_ERR_INVALID_ARG;
   }
   const hswa_pool_desc& D = pool->desc;
   if (layer < 0 || layer >= D.n_swa_layers) {
-    set_error("swa_prefill_fwd: layer %d is not a sliding-window layer of this pool", layer);
+    set_error("%s: layer %d is not a sliding-window layer of this pool", who, layer);
     return HSWA_ERR_INVALID_ARG;
   }
   int rc = check_heads(pool, n_q_heads);
   if (rc) return rc;
-  if ((rc = check_device(pool, "swa_prefill_fwd"))) return rc;
+  if ((rc = check_device(pool, who))) return rc;
   if (B < 0 || n_q < 0 || B > 65535) {
-    set_error("swa_prefill_fwd: bad B or n_q");
+    set_error("%s: bad B or n_q", who);
     return HSWA_ERR_INVALID_ARG;
   }
   if (B == 0 || n_q == 0) return HSWA_OK;
   if (!q || !k || !v || !o || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) {
-    set_error("swa_prefill_fwd: missing or misaligned tensor pointer");
+    set_error("%s: missing or misaligned tensor pointer", who);
     return HSWA_ERR_INVALID_ARG;
   }
   if (start_pos && !seq_ids) {
-    set_error("swa_prefill_fwd: seq_ids are required with start_pos");
+    set_error("%s: seq_ids are required with start_pos", who);
     return HSWA_ERR_INVALID_ARG;
   }
-  if (pool->i4 && start_pos) {
-    set_error("swa_prefill_fwd: a prefix in a 4-bit ring is not read");
-    return HSWA_ERR_UNSUPPORTED_SHAPE;
-  }
-  if (D.window == 1)  // the window is the diagonal alone: o_i = v_i
+  if (mod && (rc = check_mod_workspace(mod, B, n_q, workspace, ws_bytes, who))) return rc;
+  if (!mod && D.window == 1)  // the window is the diagonal alone: o_i = v_i
     return launch_window1(pool, v, o, B, n_q, n_q_heads, D.n_kv_heads, D.head_dim, static_cast<cudaStream_t>(stream));
   PrefillLaunch L{};
   L.B = B;
@@ -558,6 +580,8 @@ int swa_prefill_fwd(hswa_pool* pool, int layer, const hswa_bf16* q, const hswa_b
   L.pool = pool;
   L.ring_layer = layer;
   L.layer = layer;
+  L.mod = mod;
+  L.workspace = workspace;
   if ((rc = build_q_map(&L.tm_q, q, B, n_q, n_q_heads, D.head_dim))) return rc;
   if ((rc = build_q_map(&L.tm_k, k, B, n_q, D.n_kv_heads, D.head_dim))) return rc;
   if ((rc = build_q_map(&L.tm_v, v, B, n_q, D.n_kv_heads, D.head_dim))) return rc;
@@ -565,35 +589,60 @@ int swa_prefill_fwd(hswa_pool* pool, int layer, const hswa_bf16* q, const hswa_b
   return launch_prefill(L, static_cast<cudaStream_t>(stream));
 }
 
-int full_prefill_fwd(hswa_pool* pool, int layer, const hswa_bf16* q, hswa_bf16* o, int B, int n_q,
-                     const int64_t* start_pos, const int32_t* page_table, int pt_stride, int n_q_heads,
-                     void* stream) {
+int swa_prefill_fwd(hswa_pool* pool, int layer, const hswa_bf16* q, const hswa_bf16* k, const hswa_bf16* v,
+                    hswa_bf16* o, int B, int n_q, const int64_t* start_pos, const int32_t* seq_ids, int n_q_heads,
+                    void* stream) {
+  return swa_prefill("swa_prefill_fwd", pool, layer, q, k, v, o, B, n_q, start_pos, seq_ids, n_q_heads, nullptr,
+                     nullptr, 0, stream);
+}
+
+int swa_prefill_mod_fwd(hswa_pool* pool, int layer, const hswa_bf16* q, const hswa_bf16* k, const hswa_bf16* v,
+                        hswa_bf16* o, int B, int n_q, const int64_t* start_pos, const int32_t* seq_ids, int n_q_heads,
+                        const hswa_score_mod* mod, void* workspace, size_t ws_bytes, void* stream) {
+  if (int rc = check_mod(mod, "swa_prefill_mod_fwd")) return rc;
+  return swa_prefill("swa_prefill_mod_fwd", pool, layer, q, k, v, o, B, n_q, start_pos, seq_ids, n_q_heads, mod,
+                     workspace, ws_bytes, stream);
+}
+
+int prefill_mod_workspace_size(const hswa_pool* pool, int B, int n_q, size_t* bytes) {
+  if (!pool || !bytes || B < 0 || n_q < 0) {
+    set_error("prefill_mod_workspace_size: bad arguments");
+    return HSWA_ERR_INVALID_ARG;
+  }
+  *bytes = prefill_mod_bytes(B, n_q);
+  return HSWA_OK;
+}
+
+static int full_prefill(const char* who, hswa_pool* pool, int layer, const hswa_bf16* q, hswa_bf16* o, int B, int n_q,
+                        const int64_t* start_pos, const int32_t* page_table, int pt_stride, int n_q_heads,
+                        const hswa_score_mod* mod, void* workspace, size_t ws_bytes, void* stream) {
   if (!pool) {
-    set_error("full_prefill_fwd: null pool");
+    set_error("%s: null pool", who);
     return HSWA_ERR_INVALID_ARG;
   }
   const hswa_pool_desc& D = pool->desc;
   if (layer < D.n_swa_layers || layer >= D.n_swa_layers + D.n_full_layers) {
-    set_error("full_prefill_fwd: layer %d is not a full layer of this pool", layer);
+    set_error("%s: layer %d is not a full layer of this pool", who, layer);
     return HSWA_ERR_INVALID_ARG;
   }
   int rc = check_heads(pool, n_q_heads);
   if (rc) return rc;
-  if ((rc = check_device(pool, "full_prefill_fwd"))) return rc;
+  if ((rc = check_device(pool, who))) return rc;
   if (pool->fp8 && D.head_dim != 128) {
-    set_error("full_prefill_fwd: FP8 pages are read with head_dim 128 only");
+    set_error("%s: FP8 pages are read with head_dim 128 only", who);
     return HSWA_ERR_UNSUPPORTED_SHAPE;
   }
   if (B < 0 || n_q < 0 || B > 65535) {
-    set_error("full_prefill_fwd: bad B or n_q");
+    set_error("%s: bad B or n_q", who);
     return HSWA_ERR_INVALID_ARG;
   }
   if (B == 0 || n_q == 0) return HSWA_OK;
   if (!q || !o || !aligned16(q) || !aligned16(o) || !page_table || pt_stride < 1 ||
-      !(pool->fp8 ? pool->page_tma8 : pool->page_tma)) {
-    set_error("full_prefill_fwd: missing tensor pointer, page table, or pool pages");
+      !(pool->i4 ? pool->bytes_full > 0 : pool->fp8 ? pool->page_tma8 : pool->page_tma)) {
+    set_error("%s: missing tensor pointer, page table, or pool pages", who);
     return HSWA_ERR_INVALID_ARG;
   }
+  if (mod && (rc = check_mod_workspace(mod, B, n_q, workspace, ws_bytes, who))) return rc;
   PrefillLaunch L{};
   L.B = B;
   L.n_q = n_q;
@@ -608,11 +657,29 @@ int full_prefill_fwd(hswa_pool* pool, int layer, const hswa_bf16* q, hswa_bf16* 
   L.pool = pool;
   L.full_layer = layer - D.n_swa_layers;
   L.layer = layer;
+  L.mod = mod;
+  L.workspace = workspace;
   if ((rc = build_q_map(&L.tm_q, q, B, n_q, n_q_heads, D.head_dim))) return rc;
-  L.tm_k = pool->fp8 ? pool->tm_page_k8 : pool->tm_page_k;
-  L.tm_v = pool->fp8 ? pool->tm_page_v8 : pool->tm_page_v;
+  // (a 4-bit pool's pages are copied without a map; the kernel then does not use these)
+  L.tm_k = pool->i4 ? L.tm_q : pool->fp8 ? pool->tm_page_k8 : pool->tm_page_k;
+  L.tm_v = pool->i4 ? L.tm_q : pool->fp8 ? pool->tm_page_v8 : pool->tm_page_v;
   if ((rc = build_o_map(&L.tm_o, o, B, n_q, n_q_heads, D.head_dim))) return rc;
   return launch_prefill(L, static_cast<cudaStream_t>(stream));
+}
+
+int full_prefill_fwd(hswa_pool* pool, int layer, const hswa_bf16* q, hswa_bf16* o, int B, int n_q,
+                     const int64_t* start_pos, const int32_t* page_table, int pt_stride, int n_q_heads,
+                     void* stream) {
+  return full_prefill("full_prefill_fwd", pool, layer, q, o, B, n_q, start_pos, page_table, pt_stride, n_q_heads,
+                      nullptr, nullptr, 0, stream);
+}
+
+int full_prefill_mod_fwd(hswa_pool* pool, int layer, const hswa_bf16* q, hswa_bf16* o, int B, int n_q,
+                         const int64_t* start_pos, const int32_t* page_table, int pt_stride, int n_q_heads,
+                         const hswa_score_mod* mod, void* workspace, size_t ws_bytes, void* stream) {
+  if (int rc = check_mod(mod, "full_prefill_mod_fwd")) return rc;
+  return full_prefill("full_prefill_mod_fwd", pool, layer, q, o, B, n_q, start_pos, page_table, pt_stride, n_q_heads,
+                      mod, workspace, ws_bytes, stream);
 }
 
 int hybrid_decode_workspace_size(const hswa_pool* pool, int n_seqs, int n_q_per_seq, int n_q_heads,
@@ -732,18 +799,6 @@ int hybrid_decode_fwd(hswa_pool* pool, int layer, const hswa_bf16* q, const hswa
   L.workspace = workspace;
   L.ws_bytes = ws_bytes;
   return launch_decode(L, static_cast<cudaStream_t>(stream));
-}
-
-static int check_mod(const hswa_score_mod* mod, const char* who) {
-  if (!mod) {
-    set_error("%s: null score modifications", who);
-    return HSWA_ERR_INVALID_ARG;
-  }
-  if (!(mod->softcap >= 0.0f) || !isfinite(mod->softcap)) {
-    set_error("%s: softcap must be 0 or finite and > 0", who);
-    return HSWA_ERR_INVALID_ARG;
-  }
-  return HSWA_OK;
 }
 
 int hybrid_decode_mod_fwd(hswa_pool* pool, int layer, const hswa_bf16* q, const hswa_bf16* k_new,

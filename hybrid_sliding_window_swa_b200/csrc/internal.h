@@ -113,7 +113,14 @@ struct PrefillLaunch {
   // tensor maps built by the ABI layer
   CUtensorMap tm_q, tm_k, tm_v;  // tm_k/tm_v: chunk K/V (SWA) or pages (full)
   CUtensorMap tm_o;              // output, stored 32 rows x 64 columns per TMA box
+  const hswa_score_mod* mod;     // null: plain scores
+  void* workspace;               // with key ranges: prefill_mod_bytes(B, n_q)
 };
+
+// Workspace of a prefill with key ranges: per query tile its bounds (16 bytes) and its place in the order.
+inline size_t prefill_mod_bytes(int B, int n_q) {
+  return (((size_t)B * (((size_t)n_q + 127) / 128) * 20) + 255) & ~(size_t)255;
+}
 
 int launch_prefill(const PrefillLaunch& L, cudaStream_t stream);
 // Sliding-window prefill with 1 <= W <= 129 (the band of a query tile spans at most two key tiles).

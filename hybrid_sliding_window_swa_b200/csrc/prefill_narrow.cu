@@ -56,6 +56,7 @@ struct NParams {
   const float* k_scale;
   const float* v_scale;
   int fp8;
+  int64_t ring_blk;  // 4-bit pools: bytes of a ring block
   int ring_layer, n_swa, max_seqs, ring_tma;
   float scale_log2;
   int n_tiles;  // query tiles per batch row
@@ -190,7 +191,7 @@ __device__ __forceinline__ float softmax_band(uint32_t trow, uint32_t s_col, int
 
 // ---------------------------------------------------------------- K/V producer
 
-template <int D>
+template <int D, bool I4>
 __device__ void kv_producer(const NParams& p, uint8_t* smem, NBars* bars, const CUtensorMap* tm_k,
                             const CUtensorMap* tm_v, const CUtensorMap* tm_rk, const CUtensorMap* tm_rv) {
   using L = NLayout<D>;
@@ -218,7 +219,10 @@ __device__ void kv_producer(const NParams& p, uint8_t* smem, NBars* bars, const 
         if (!seq_ok && lane == 0) record_error(p.err, HSWA_ERR_DEVICE_BOUNDS);
         const int held_lo = (G.P - p.window > 0) ? G.P - p.window : 0;
         const int64_t base = ring_row * p.window * D;
-        if (p.fp8)
+        if constexpr (I4)
+          ring_rows_i4<D>((kv ? p.ring_v8 : p.ring_k8) + ring_row * p.ring_blk, seq_ok, held_lo, G.P, p.window, dst0,
+                          G.P + BN * j0, lane, blk_stride);
+        else if (p.fp8)
           ring_rows_fp8<D>((kv ? p.ring_v8 : p.ring_k8) + base, seq_ok, held_lo, G.P, p.window,
                            kv ? p.v_scale[G.g] : p.k_scale[G.g], dst0, G.P + BN * j0, lane, blk_stride);
         else
@@ -389,7 +393,7 @@ __device__ void softmax_slot(const NParams& p, uint8_t* smem, NBars* bars, uint3
   }
 }
 
-template <int D>
+template <int D, bool I4>
 __global__ void __launch_bounds__(NTHREADS, 1)
     prefill_narrow_kernel(const __grid_constant__ NParams p, const __grid_constant__ CUtensorMap tm_q,
                           const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -439,7 +443,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 " HSWA_STR(HSWA_PRODUCER_REGS) ";" ::: "memory");
     if (warp == KV_WARP) {
-      kv_producer<D>(p, smem, bars, &tm_k, &tm_v, &tm_rk, &tm_rv);
+      kv_producer<D, I4>(p, smem, bars, &tm_k, &tm_v, &tm_rk, &tm_rv);
     } else if ((threadIdx.x & 31) == 0) {
       if (warp == MMA_WARP) mma_issuer<D>(p, smem, bars, tbase);
       else if (warp == QP_WARP) q_producer<D>(p, smem, bars, &tm_q);
@@ -478,6 +482,7 @@ int launch_prefill_narrow(const PrefillLaunch& Lc, cudaStream_t stream) {
   p.ring_k8 = pool->ring_k8;
   p.ring_v8 = pool->ring_v8;
   p.fp8 = pool->fp8 ? 1 : 0;
+  p.ring_blk = pool->ring_blk;
   if (pool->fp8) {
     const int n_layers = D.n_swa_layers + D.n_full_layers;
     p.k_scale = pool->scales + (size_t)(0 * n_layers + Lc.layer) * D.n_kv_heads;
@@ -503,15 +508,20 @@ int launch_prefill_narrow(const PrefillLaunch& Lc, cudaStream_t stream) {
 
   const CUtensorMap& rk = pool->ring_tma ? pool->tm_ring_k : Lc.tm_k;
   const CUtensorMap& rv = pool->ring_tma ? pool->tm_ring_v : Lc.tm_v;
-  if (Lc.d == 128) {
-    const int smem = NLayout<128>::BYTES + 1024;
-    cudaFuncSetAttribute(prefill_narrow_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    prefill_narrow_kernel<128><<<grid, NTHREADS, smem, stream>>>(p, Lc.tm_q, Lc.tm_k, Lc.tm_v, rk, rv, Lc.tm_o);
+  const int smem = (Lc.d == 128 ? NLayout<128>::BYTES : NLayout<64>::BYTES) + 1024;
+#define HSWA_NARROW(DD, I4_)                                                                                         \
+  do {                                                                                                               \
+    cudaFuncSetAttribute(prefill_narrow_kernel<DD, I4_>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);         \
+    prefill_narrow_kernel<DD, I4_><<<grid, NTHREADS, smem, stream>>>(p, Lc.tm_q, Lc.tm_k, Lc.tm_v, rk, rv, Lc.tm_o); \
+  } while (0)
+  if (pool->i4) {
+    if (Lc.d == 128) HSWA_NARROW(128, true);
+    else HSWA_NARROW(64, true);
   } else {
-    const int smem = NLayout<64>::BYTES + 1024;
-    cudaFuncSetAttribute(prefill_narrow_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    prefill_narrow_kernel<64><<<grid, NTHREADS, smem, stream>>>(p, Lc.tm_q, Lc.tm_k, Lc.tm_v, rk, rv, Lc.tm_o);
+    if (Lc.d == 128) HSWA_NARROW(128, false);
+    else HSWA_NARROW(64, false);
   }
+#undef HSWA_NARROW
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {
     set_error("prefill: launch failed: %s", cudaGetErrorString(e));

@@ -42,6 +42,7 @@
 // absolute positions [128 j, 128 j + 128) = two 64-token pages.
 #include "common.cuh"
 #include "internal.h"
+#include "kv_quant.cuh"
 #include "prefill_tile.cuh"
 
 namespace hswa {
@@ -82,7 +83,131 @@ struct Params {
   int n_units;
   int64_t max_start;  // largest start position that keeps every position below 2^31
   int* err;
+  // 4-bit pools
+  int64_t blk_bytes;  // bytes of a ring block (SWA) or page block (full)
+  const uint8_t* page_k8;
+  const uint8_t* page_v8;
+  // modified scores
+  ScoreParams sp;
+  const int4* bounds;  // [B][n_tiles] of the key ranges (see bounds_kernel), or null (causal)
+  const int* order;    // unit order over (batch row, tile) or (batch row, tile pair) entries
 };
+
+// Keys the query of chunk row r (position P + r) sees, [lo, hi); hi <= lo: none. Positions at or past
+// the end of the chunk do not exist; a sliding window bounds both sides.
+__device__ __forceinline__ void mod_row_range(const Params& p, int b, int P, int r, int& lo, int& hi) {
+  const int64_t i = (int64_t)P + r;
+  int64_t a = 0, e = i + 1;
+  if (r >= p.n_q) {
+    lo = hi = 0;
+    return;
+  }
+  const int64_t idx = (int64_t)b * p.n_q + r;
+  if (p.sp.key_end) e = min(p.sp.key_end[idx], (int64_t)P + p.n_q);
+  if (p.sp.key_begin) a = max(p.sp.key_begin[idx], (int64_t)0);
+  if (p.window > 0) {
+    a = max(a, i - p.window + 1);
+    e = min(e, i + p.window);
+  }
+  e = max(e, (int64_t)0);
+  if (a > e) a = e;
+  lo = (int)a;
+  hi = (int)e;
+}
+
+__device__ __forceinline__ int chunk_start(const Params& p, int b) {
+  const int64_t P = p.start_pos ? p.start_pos[b] : 0;
+  if (P < 0 || P > p.max_start) {  // positions must stay below 2^31
+    record_error(p.err, HSWA_ERR_DEVICE_BOUNDS);
+    return 0;
+  }
+  return (int)P;
+}
+
+// Key ranges of the query tiles: one warp per (batch row, tile) writes (x, y) = the union [lo, hi) of its
+// rows' ranges (0, 0 when no row sees a key) and (z, w) = their intersection, inside which no row of the
+// tile needs a mask. An empty row makes the intersection empty.
+__global__ void __launch_bounds__(256) bounds_kernel(Params p, int4* out) {
+  const int e = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (e >= p.B * p.n_tiles) return;
+  const int b = e / p.n_tiles, t = e - b * p.n_tiles;
+  const int P = chunk_start(p, b);
+  int lo = 0x7fffffff, hi = 0, zlo = 0, zhi = 0x7fffffff;
+#pragma unroll
+  for (int k = 0; k < BM / 32; ++k) {
+    const int r = t * BM + k * 32 + lane;
+    if (r >= p.n_q) continue;
+    int a, c;
+    mod_row_range(p, b, P, r, a, c);
+    if (c > a) {
+      lo = min(lo, a);
+      hi = max(hi, c);
+    }
+    zlo = max(zlo, a);
+    zhi = min(zhi, c);
+  }
+#pragma unroll
+  for (int x = 16; x; x >>= 1) {
+    lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, x));
+    hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, x));
+    zlo = max(zlo, __shfl_xor_sync(0xffffffffu, zlo, x));
+    zhi = min(zhi, __shfl_xor_sync(0xffffffffu, zhi, x));
+  }
+  if (lane == 0) out[e] = hi > lo ? make_int4(lo, hi, zlo, zhi) : make_int4(0, 0, 0, 0);
+}
+
+// The entries (tiles, or pairs of tiles for odd G) by falling number of key tiles, so that the rounds of
+// the persistent loop hand out units of like size: a counting sort by one block. Entries of one size
+// come in any order, which changes the schedule but no result.
+constexpr int ORDER_BINS = 1024;
+__global__ void __launch_bounds__(1024) order_kernel(Params p, const int4* bounds, int* order) {
+  __shared__ int bins[ORDER_BINS];
+  __shared__ int warp_sum[32];
+  const int per = p.head_pairs ? p.n_tiles : p.n_pairs;
+  const int n = p.B * per;
+  auto size_bin = [&](int e) {
+    const int b = e / per, t = e - b * per;
+    int lo = 0x7fffffff, hi = 0;
+    for (int q = 0; q < (p.head_pairs ? 1 : NQT); ++q) {
+      const int tt = p.head_pairs ? t : t * NQT + q;
+      if (tt >= p.n_tiles) continue;
+      const int4 x = bounds[b * p.n_tiles + tt];
+      if (x.y > x.x) {
+        lo = min(lo, x.x);
+        hi = max(hi, x.y);
+      }
+    }
+    const int size = hi > lo ? (hi - lo + BN - 1) / BN : 0;
+    return ORDER_BINS - 1 - min(size, ORDER_BINS - 1);  // largest first
+  };
+  bins[threadIdx.x] = 0;
+  __syncthreads();
+  for (int e = threadIdx.x; e < n; e += 1024) atomicAdd(&bins[size_bin(e)], 1);
+  __syncthreads();
+  const int v = bins[threadIdx.x], lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, s);
+    if (lane >= s) x += y;
+  }
+  if (lane == 31) warp_sum[w] = x;
+  __syncthreads();
+  if (w == 0) {
+    int z = warp_sum[lane];
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, z, s);
+      if (lane >= s) z += y;
+    }
+    warp_sum[lane] = z;
+  }
+  __syncthreads();
+  bins[threadIdx.x] = x - v + (w > 0 ? warp_sum[w - 1] : 0);
+  __syncthreads();
+  for (int e = threadIdx.x; e < n; e += 1024) order[atomicAdd(&bins[size_bin(e)], 1)] = e;
+}
 
 template <int D>
 struct Layout {
@@ -105,6 +230,7 @@ struct Bars {
   uint64_t raw_k[NSTAGE], raw_v[NSTAGE];  // FP8 page tiles landed (before conversion)
   uint64_t s_full[NQT], p_full[NQT], o_full[NQT];
   uint64_t v_fix;  // TMA completion of the page tile that holds the last key (before its tail is zeroed)
+  uint32_t half_ok[2][NSTAGE];  // 4-bit pages: which 64-row halves of a raw tile (K, V) were copied
   uint32_t tmem_base;
 };
 
@@ -119,6 +245,8 @@ struct Geo {
   int i0[NQT], i1[NQT];  // first / last valid absolute query position of each tile
   int jlo[NQT], jhi[NQT];
   int jb, je;            // union of needed key tiles, inclusive
+  int kmin, kmax;        // smallest and largest key position any query of the unit sees
+  int zlo[NQT], zhi[NQT];  // modified scores: every row of the tile sees [zlo, zhi)
 };
 
 __device__ __forceinline__ int window_lo(const Params& p, int i) {
@@ -156,10 +284,26 @@ __device__ __forceinline__ int cta_unit(int r) {
   return r * (int)gridDim.x + c;
 }
 
+template <bool MOD>
 __device__ __forceinline__ void make_geo(const Params& p, int unit, Geo& G) {
   int tq[NQT];
   int t, bg, in;
-  if (p.head_pairs) {
+  if (MOD && p.bounds) {
+    // units of one entry (its heads) are consecutive
+    const int n_in = p.head_pairs ? p.G >> 1 : p.G;
+    const int per_entry = p.Hkv * n_in;
+    const int k = unit / per_entry, rem = unit - k * per_entry;
+    const int e = p.order[k], per = p.head_pairs ? p.n_tiles : p.n_pairs;
+    G.b = e / per;
+    t = e - G.b * per;
+    G.g = rem / n_in;
+    in = rem - G.g * n_in;
+#pragma unroll
+    for (int q = 0; q < NQT; ++q) {
+      tq[q] = p.head_pairs ? t : t * NQT + q;
+      G.hq[q] = p.head_pairs ? G.g * p.G + 2 * in + q : G.g * p.G + in;
+    }
+  } else if (p.head_pairs) {
     unit_order(unit, p.n_tiles, p.B * p.Hkv, p.G >> 1, p.t_block, t, bg, in);
     G.b = bg / p.Hkv;
     G.g = bg - G.b * p.Hkv;
@@ -178,14 +322,11 @@ __device__ __forceinline__ void make_geo(const Params& p, int unit, Geo& G) {
       G.hq[q] = G.g * p.G + in;
     }
   }
-  int64_t P = p.start_pos ? p.start_pos[G.b] : 0;
-  if (P < 0 || P > p.max_start) {  // positions must stay below 2^31
-    record_error(p.err, HSWA_ERR_DEVICE_BOUNDS);
-    P = 0;
-  }
-  G.P = (int)P;
+  G.P = chunk_start(p, G.b);
   G.jb = INT32_MAX;
   G.je = INT32_MIN;
+  G.kmin = MOD ? INT32_MAX : 0;
+  G.kmax = MOD ? -1 : 0;
 #pragma unroll
   for (int q = 0; q < NQT; ++q) {
     G.t[q] = tq[q];
@@ -197,6 +338,29 @@ __device__ __forceinline__ void make_geo(const Params& p, int unit, Geo& G) {
     const int r1 = (r0 + BM - 1 < p.n_q - 1) ? r0 + BM - 1 : p.n_q - 1;
     G.i0[q] = G.P + r0;
     G.i1[q] = G.P + r1;
+    if constexpr (MOD) {
+      int4 x;
+      if (p.bounds) {
+        x = p.bounds[G.b * p.n_tiles + tq[q]];
+      } else {
+        x.x = window_lo(p, G.i0[q]);
+        x.y = G.i1[q] + 1;
+        x.z = window_lo(p, G.i1[q]);
+        x.w = G.i0[q] + 1;
+      }
+      G.zlo[q] = x.z;
+      G.zhi[q] = x.w;
+      if (x.y <= x.x) continue;  // no row sees a key
+      const int base = p.is_full ? 0 : G.P;
+      G.jlo[q] = floordiv(x.x - base, BN);
+      G.jhi[q] = floordiv(x.y - 1 - base, BN);
+      G.kmin = min(G.kmin, x.x);
+      G.kmax = max(G.kmax, x.y - 1);
+      G.jb = min(G.jb, G.jlo[q]);
+      G.je = max(G.je, G.jhi[q]);
+      continue;
+    }
+    if (G.i1[q] > G.kmax) G.kmax = G.i1[q];
     if (p.is_full) {
       G.jlo[q] = 0;
       G.jhi[q] = floordiv(G.i1[q], BN);
@@ -215,17 +379,39 @@ __device__ __forceinline__ bool needs(const Geo& G, int q, int j) {
 
 // ---------------------------------------------------------------- producer
 
+// Zero the rows of a V tile outside positions [kmin, kmax] (one warp; the swizzle permutes the chunks of
+// a row among themselves).
+template <int D>
+__device__ __forceinline__ void zero_rows(uint8_t* dst, int kb, int kmin, int kmax, int lane) {
+  for (int idx = lane; idx < BN * (D / 8); idx += 32) {
+    const int r = idx / (D / 8), c = idx % (D / 8);
+    if (kb + r < kmin || kb + r > kmax)
+      *reinterpret_cast<uint4*>(dst + (c >> 3) * Layout<D>::BLOCK + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+  }
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
 // Rolling-buffer rows of one key tile with cp.async (general W and chunk start):
 // rows whose position is not held by the ring (or is negative) are zero-filled.
-template <int D>
+template <int D, bool I4, bool MOD>
 __device__ __forceinline__ void ring_tile_cpasync(const Params& p, const Geo& G, const uint16_t* ring,
                                                   uint8_t* dst, int kb, int lane) {
   const int seq = p.seq_ids ? p.seq_ids[G.b] : 0;
   const bool seq_ok = seq >= 0 && seq < p.max_seqs;
   if (!seq_ok && lane == 0) record_error(p.err, HSWA_ERR_DEVICE_BOUNDS);
   const int64_t row_base = seq_ok ? (((int64_t)seq * p.n_swa + p.ring_layer) * p.Hkv + G.g) * p.window : 0;
-  const int held_lo = (G.P - p.window > 0) ? G.P - p.window : 0;
-  if (p.fp8) {
+  int held_lo = (G.P - p.window > 0) ? G.P - p.window : 0;
+  if constexpr (MOD) held_lo = max(held_lo, G.kmin);  // rows no query of the unit sees are not read
+  if constexpr (I4) {
+    const int64_t blk = seq_ok ? (((int64_t)seq * p.n_swa + p.ring_layer) * p.Hkv + G.g) * p.blk_bytes : 0;
+    ring_rows_i4<D>((ring == p.ring_v ? p.ring_v8 : p.ring_k8) + blk, seq_ok, held_lo, G.P, p.window, dst, kb, lane);
+  } else if (p.fp8) {
     const bool is_v = ring == p.ring_v;
     ring_rows_fp8<D>((is_v ? p.ring_v8 : p.ring_k8) + row_base * D, seq_ok, held_lo, G.P, p.window,
                      is_v ? p.v_scale[G.g] : p.k_scale[G.g], dst, kb, lane);
@@ -241,7 +427,7 @@ __device__ __forceinline__ void ring_tile_cpasync(const Params& p, const Geo& G,
 // reads them before it writes). Values are code value times the KV head's scale, rounded to bf16.
 // Rows past the last key of the unit are written as zeros. Then the buffer is handed to the MMA
 // (k_full / v_full, one arrival per converting thread).
-template <int D>
+template <int D, bool MOD>
 __device__ void page_converter(const Params& p, uint8_t* smem, Bars* bars) {
   using L = Layout<D>;
   static_assert(D == 128, "FP8 page tiles are converted for head_dim 128");
@@ -249,10 +435,8 @@ __device__ void page_converter(const Params& p, uint8_t* smem, Bars* bars) {
   int it = 0;
   for (int rnd = 0, unit = cta_unit(0); unit < p.n_units; unit = cta_unit(++rnd)) {
     Geo G;
-    make_geo(p, unit, G);
-    int kmax = 0;
-    for (int q = 0; q < NQT; ++q)
-      if (G.act[q] && G.i1[q] > kmax) kmax = G.i1[q];
+    make_geo<MOD>(p, unit, G);
+    const int kmin = G.kmin, kmax = G.kmax;
     for (int j = G.jb; j <= G.je; ++j, ++it) {
       const int s = it % NSTAGE;
       const uint32_t ph = (it / NSTAGE) & 1;
@@ -264,7 +448,7 @@ __device__ void page_converter(const Params& p, uint8_t* smem, Bars* bars) {
 #pragma unroll 1
         for (int rr = 0; rr < 2; ++rr) {
           const int r = ct + 64 * rr;
-          const bool zero = kb + r > kmax;
+          const bool zero = kb + r > kmax || (MOD && kb + r < kmin);
           const int sw = r & 7;
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
@@ -299,7 +483,68 @@ __device__ void page_converter(const Params& p, uint8_t* smem, Bars* bars) {
   }
 }
 
-template <int D>
+// 4-bit page tiles (full layers of a 4-bit pool): the producer copies the two page blocks of a tile (64
+// rows of codes and their pairs, contiguous in HBM, one bulk copy each) into the stage buffer; warp
+// 10 + h turns half h into bf16. The raw block lies in the 8 KB of the buffer that the half's own upper
+// (head_dim 64: only) block rows take afterwards, so a warp reads its rows' codes and pairs into registers
+// (two rows per lane), meets at the warp barrier, and then writes; the two halves do not touch. Six
+// instructions per pair of values, about 1500 per lane and pair of K and V tiles, in the shadow of the
+// tile's MMAs and softmax. Rows no query of the unit sees, and those of a bad page, become zeros.
+template <int D, bool MOD>
+__device__ void page_converter_i4(const Params& p, uint8_t* smem, Bars* bars) {
+  using L = Layout<D>;
+  constexpr int NC = D / 32;  // 16-byte chunks of codes per row
+  const int lane = threadIdx.x & 31;
+  const int half = (threadIdx.x >> 5) - 10;
+  int it = 0;
+  for (int rnd = 0, unit = cta_unit(0); unit < p.n_units; unit = cta_unit(++rnd)) {
+    Geo G;
+    make_geo<MOD>(p, unit, G);
+    for (int j = G.jb; j <= G.je; ++j, ++it) {
+      const int s = it % NSTAGE;
+      const uint32_t ph = (it / NSTAGE) & 1;
+      const int kb = key_base(p, G, j) + 64 * half;
+      for (int kv = 0; kv < 2; ++kv) {
+        if (!mbar_wait(kv ? &bars->raw_v[s] : &bars->raw_k[s], ph, p.err)) return;
+        uint8_t* tile = smem + (kv ? L::V_OFF : L::K_OFF) + s * L::TILE;
+        const uint8_t* raw = tile + (D / 64 - 1) * L::BLOCK + half * 8192;
+        const bool ok = (bars->half_ok[kv][s] >> half) & 1;
+        uint4 x[2][NC];
+        uint32_t pr[2];
+#pragma unroll
+        for (int rr = 0; rr < 2; ++rr) {
+          const int r = lane + 32 * rr;
+          const bool live = ok && kb + r <= G.kmax && (!MOD || kb + r >= G.kmin);
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+            x[rr][c] = live ? reinterpret_cast<const uint4*>(raw + r * (D / 2))[c] : make_uint4(0, 0, 0, 0);
+          pr[rr] = live ? reinterpret_cast<const uint32_t*>(raw + 64 * (D / 2))[r] : 0u;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int rr = 0; rr < 2; ++rr) {
+          const int r = 64 * half + lane + 32 * rr;
+          __nv_bfloat162 step, lo;
+          i4_pair_bf162(pr[rr], step, lo);
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const uint32_t w[4] = {x[rr][c].x, x[rr][c].y, x[rr][c].z, x[rr][c].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int cc = 4 * c + i;
+              *reinterpret_cast<uint4*>(tile + (cc >> 3) * L::BLOCK + r * 128 + (((cc & 7) ^ (r & 7)) << 4)) =
+                  i4x8_bf16(w[i], step, lo);
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(kv ? &bars->v_full[s] : &bars->k_full[s]);
+      }
+    }
+  }
+}
+
+template <int D, bool I4, bool MOD>
 __device__ void producer(const Params& p, uint8_t* smem, Bars* bars, const CUtensorMap* tm_q,
                          const CUtensorMap* tm_k, const CUtensorMap* tm_v, const CUtensorMap* tm_rk,
                          const CUtensorMap* tm_rv) {
@@ -310,7 +555,7 @@ __device__ void producer(const Params& p, uint8_t* smem, Bars* bars, const CUten
   uint32_t nfix = 0; // page tiles zero-filled past the last key (v_fix phase)
   for (int rnd = 0, unit = cta_unit(0); unit < p.n_units; unit = cta_unit(++rnd), ++uq) {
     Geo G;
-    make_geo(p, unit, G);
+    make_geo<MOD>(p, unit, G);
     // the Q buffers are free once every S MMA of the previous unit has completed
     if (!mbar_wait(&bars->q_empty, (uq & 1) ^ 1, p.err)) return;
     if (lane == 0) {
@@ -325,10 +570,8 @@ __device__ void producer(const Params& p, uint8_t* smem, Bars* bars, const CUten
       }
     }
     __syncwarp();
-    // highest key position any query of this unit may need
-    int kmax = 0;
-    for (int q = 0; q < NQT; ++q)
-      if (G.act[q] && G.i1[q] > kmax) kmax = G.i1[q];
+    // lowest and highest key position any query of this unit may need
+    const int kmin = G.kmin, kmax = G.kmax;
     const int seq = (!p.is_full && p.seq_ids) ? p.seq_ids[G.b] : 0;
     const bool ring_fast = p.ring_tma && (G.P % BN) == 0;
 
@@ -341,6 +584,36 @@ __device__ void producer(const Params& p, uint8_t* smem, Bars* bars, const CUten
         uint64_t* empty = kv ? &bars->v_empty[s] : &bars->k_empty[s];
         uint8_t* dst = smem + (kv ? L::V_OFF : L::K_OFF) + s * L::TILE;
         if (!mbar_wait(empty, ph ^ 1, p.err)) return;
+        if constexpr (I4) {
+          if (p.is_full) {
+            uint64_t* raw = kv ? &bars->raw_v[s] : &bars->raw_k[s];
+            if (lane == 0) {
+              int64_t blk[2];
+              uint32_t ok = 0;
+              for (int half = 0; half < 2; ++half) {
+                const int pos0 = kb + 64 * half;
+                const int lp = pos0 / 64;
+                if (pos0 > kmax || (MOD && pos0 + 63 < kmin)) continue;
+                const int32_t page = lp < p.pt_stride ? p.page_table[(int64_t)G.b * p.pt_stride + lp] : -1;
+                if (page < 0 || page >= p.pages) {
+                  record_error(p.err, HSWA_ERR_DEVICE_BOUNDS);
+                } else {
+                  blk[half] = ((int64_t)p.full_layer * p.pages + page) * p.Hkv + G.g;
+                  ok |= 1u << half;
+                }
+              }
+              bars->half_ok[kv][s] = ok;
+              mbar_arrive_expect_tx(raw, __popc(ok) * (uint32_t)i4_block_bytes(64, D));
+              for (int half = 0; half < 2; ++half)
+                if ((ok >> half) & 1)
+                  bulk_load(dst + (D / 64 - 1) * L::BLOCK + half * 8192,
+                            (kv ? p.page_v8 : p.page_k8) + blk[half] * i4_block_bytes(64, D),
+                            (uint32_t)i4_block_bytes(64, D), raw);
+            }
+            __syncwarp();
+            continue;
+          }
+        }
         if (p.is_full && p.conv) {
           // FP8 pages: the codes go to the upper half of the stage buffer; page_converter makes bf16
           uint64_t* raw = kv ? &bars->raw_v[s] : &bars->raw_k[s];
@@ -351,7 +624,7 @@ __device__ void producer(const Params& p, uint8_t* smem, Bars* bars, const CUten
               const int pos0 = kb + 64 * half;
               const int lp = pos0 / 64;
               int64_t row = -1;  // outside the map: zero fill
-              if (pos0 <= kmax) {
+              if (pos0 <= kmax && (!MOD || pos0 + 63 >= kmin)) {
                 int32_t page = -1;
                 if (lp < p.pt_stride) page = p.page_table[(int64_t)G.b * p.pt_stride + lp];
                 if (page < 0 || page >= p.pages) {
@@ -366,7 +639,9 @@ __device__ void producer(const Params& p, uint8_t* smem, Bars* bars, const CUten
         } else if (p.is_full) {
           // Rows of the last page past the last key hold stale memory; P is 0 there, but
           // 0 * NaN would still poison P V, so that V tile is zeroed past kmax before use.
-          const bool fix = kv == 1 && kb <= kmax && kmax < kb + BN - 1 && ((kmax + 1) % 64) != 0;
+          // With key ranges the same holds below the first key any query of the unit sees.
+          const bool fix = kv == 1 && ((kb <= kmax && kmax < kb + BN - 1 && ((kmax + 1) % 64) != 0) ||
+                                       (MOD && kmin > kb && kmin < kb + BN && (kmin % 64) != 0));
           uint64_t* land = fix ? &bars->v_fix : full;
           if (lane == 0) {
             mbar_arrive_expect_tx(land, L::TILE);
@@ -375,7 +650,7 @@ __device__ void producer(const Params& p, uint8_t* smem, Bars* bars, const CUten
               const int pos0 = kb + 64 * half;
               const int lp = pos0 / 64;
               int64_t row = -1;  // outside the map: zero fill
-              if (pos0 <= kmax) {
+              if (pos0 <= kmax && (!MOD || pos0 + 63 >= kmin)) {
                 int32_t page = -1;
                 if (lp < p.pt_stride) page = p.page_table[(int64_t)G.b * p.pt_stride + lp];
                 if (page < 0 || page >= p.pages) {
@@ -392,25 +667,43 @@ __device__ void producer(const Params& p, uint8_t* smem, Bars* bars, const CUten
             __syncwarp();
             if (!mbar_wait(&bars->v_fix, nfix & 1, p.err)) return;
             ++nfix;
-            const int r0 = (int)(kmax - kb + 1);
-            for (int idx = lane; idx < (BN - r0) * (D / 8); idx += 32) {
-              const int r = r0 + idx / (D / 8);
-              const int c = idx % (D / 8);
-              *reinterpret_cast<uint4*>(dst + (c >> 3) * L::BLOCK + r * 128 + (c & 7) * 16) =
-                  make_uint4(0, 0, 0, 0);
+            if constexpr (MOD) {
+              zero_rows<D>(dst, kb, kmin, kmax, lane);
+            } else {
+              const int r0 = (int)(kmax - kb + 1);
+              for (int idx = lane; idx < (BN - r0) * (D / 8); idx += 32) {
+                const int r = r0 + idx / (D / 8);
+                const int c = idx % (D / 8);
+                *reinterpret_cast<uint4*>(dst + (c >> 3) * L::BLOCK + r * 128 + (c & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
+              }
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(full);
           }
         } else if (j >= 0) {
+          // modified scores: chunk rows no query of the unit sees may hold anything (padding)
+          const bool fix = MOD && kv == 1 && ((kmin > kb && kmin < kb + BN) || (kmax >= kb && kmax < kb + BN - 1));
+          uint64_t* land = fix ? &bars->v_fix : full;
           if (lane == 0) {
-            mbar_arrive_expect_tx(full, L::TILE);
+            mbar_arrive_expect_tx(land, L::TILE);
             const CUtensorMap* tm = kv ? tm_v : tm_k;
             for (int dh = 0; dh < D / 64; ++dh)
-              tma_load_4d(dst + dh * L::BLOCK, tm, full, dh * 64, G.g, (int)(BN * j), G.b);
+              tma_load_4d(dst + dh * L::BLOCK, tm, land, dh * 64, G.g, (int)(BN * j), G.b);
           }
-        } else if (ring_fast) {
+          if constexpr (MOD) {
+            if (fix) {
+              __syncwarp();
+              if (!mbar_wait(&bars->v_fix, nfix & 1, p.err)) return;
+              ++nfix;
+              zero_rows<D>(dst, kb, kmin, kmax, lane);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(full);
+            }
+          }
+        } else if (ring_fast && (!MOD || kmin <= kb)) {
           if (lane == 0) {
             mbar_arrive_expect_tx(full, L::TILE);
             const CUtensorMap* tm = kv ? tm_rv : tm_rk;
@@ -423,7 +716,7 @@ __device__ void producer(const Params& p, uint8_t* smem, Bars* bars, const CUten
             for (int dh = 0; dh < D / 64; ++dh) tma_load_3d(dst + dh * L::BLOCK, tm, full, dh * 64, slot, row);
           }
         } else {
-          ring_tile_cpasync<D>(p, G, kv ? p.ring_v : p.ring_k, dst, kb, lane);
+          ring_tile_cpasync<D, I4, MOD>(p, G, kv ? p.ring_v : p.ring_k, dst, kb, lane);
           if (lane == 0) mbar_arrive(full);
         }
         __syncwarp();
@@ -434,7 +727,7 @@ __device__ void producer(const Params& p, uint8_t* smem, Bars* bars, const CUten
 
 // ---------------------------------------------------------------- MMA issuer
 
-template <int D>
+template <int D, bool MOD>
 __device__ void mma_issuer(const Params& p, uint8_t* smem, Bars* bars, uint32_t tbase) {
   using L = Layout<D>;
   constexpr uint32_t IDESC_S = idesc_bf16_f32(BM, BN, false);
@@ -448,7 +741,7 @@ __device__ void mma_issuer(const Params& p, uint8_t* smem, Bars* bars, uint32_t 
   uint32_t uq = 0;
   for (int rnd = 0, unit = cta_unit(0); unit < p.n_units; unit = cta_unit(++rnd), ++uq) {
     Geo G;
-    make_geo(p, unit, G);
+    make_geo<MOD>(p, unit, G);
     if (!mbar_wait(&bars->q_full, uq & 1, p.err)) return;
     tc_fence_after();
 
@@ -535,7 +828,7 @@ __device__ void mma_issuer(const Params& p, uint8_t* smem, Bars* bars, uint32_t 
 
 // ---------------------------------------------------------------- softmax + epilogue
 
-template <int D>
+template <int D, bool MOD>
 __device__ void softmax_wg(const Params& p, uint8_t* smem, Bars* bars, uint32_t tbase, const int q,
                            const CUtensorMap* tm_o) {
   using L = Layout<D>;
@@ -551,7 +844,7 @@ __device__ void softmax_wg(const Params& p, uint8_t* smem, Bars* bars, uint32_t 
 
   for (int rnd = 0, unit = cta_unit(0); unit < p.n_units; unit = cta_unit(++rnd)) {
     Geo G;
-    make_geo(p, unit, G);
+    make_geo<MOD>(p, unit, G);
     // this warpgroup's query tile, as scalars (one code path for both warpgroups)
     const bool act = q ? G.act[1] : G.act[0];
     if (!act) continue;
@@ -560,9 +853,26 @@ __device__ void softmax_wg(const Params& p, uint8_t* smem, Bars* bars, uint32_t 
     const int qjlo = q ? G.jlo[1] : G.jlo[0];
     const int qjhi = q ? G.jhi[1] : G.jhi[0];
     const int qt = q ? G.t[1] : G.t[0];
-    const int lo_last = window_lo(p, qi1);
     const int i = qi0 + r;
-    const int lo_i = window_lo(p, i);
+    int lo_last, hi_first, lo_i, hi_i;  // the tile's rows all see [lo_last, hi_first); row r sees [lo_i, hi_i]
+    float slope2 = 0.f;
+    if constexpr (MOD) {
+      lo_last = q ? G.zlo[1] : G.zlo[0];
+      hi_first = q ? G.zhi[1] : G.zhi[0];
+      if (p.bounds) {
+        mod_row_range(p, G.b, G.P, qt * BM + r, lo_i, hi_i);
+        --hi_i;
+      } else {
+        lo_i = window_lo(p, i);
+        hi_i = i;
+      }
+      if (p.sp.slope) slope2 = p.sp.slope[q ? G.hq[1] : G.hq[0]] * 1.4426950408889634f;
+    } else {
+      lo_last = window_lo(p, qi1);
+      hi_first = qi0 + 1;
+      lo_i = window_lo(p, i);
+      hi_i = i;
+    }
     float m_used = -INFINITY;
     float l = 0.f;
     uint32_t n_done = 0;
@@ -573,10 +883,14 @@ __device__ void softmax_wg(const Params& p, uint8_t* smem, Bars* bars, uint32_t 
       tc_fence_after();
       // columns of this row inside the band: [c_lo, c_hi] (edge tiles only)
       const int kb = key_base(p, G, j);
-      const bool edge = !(kb + BN - 1 <= qi0 && kb >= lo_last);
+      const bool edge = !(kb + BN <= hi_first && kb >= lo_last);
       const int c_lo = lo_i - kb;
-      const int c_hi = i - kb;
-      softmax_tile<D, 1>(trow, s_col, o_col, sl2, edge, c_lo, c_hi, m_used, l, n_done > 0);
+      const int c_hi = hi_i - kb;
+      if constexpr (MOD)
+        softmax_tile<D, 1, true>(trow, s_col, o_col, sl2, edge, c_lo, c_hi, m_used, l, n_done > 0, 0, false, &p.sp,
+                                 slope2, (float)(i - kb));
+      else
+        softmax_tile<D, 1>(trow, s_col, o_col, sl2, edge, c_lo, c_hi, m_used, l, n_done > 0);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&bars->p_full[q]);
@@ -586,7 +900,7 @@ __device__ void softmax_wg(const Params& p, uint8_t* smem, Bars* bars, uint32_t 
     if (!mbar_wait(&bars->o_full[q], no & 1, p.err)) return;
     ++no;
     tc_fence_after();
-    store_output<D>(trow, o_col, l, smem + L::O_OFF + q * L::BLOCK + wq * 4096, lane, tm_o, q ? G.hq[1] : G.hq[0],
+    store_output<D, MOD>(trow, o_col, l, smem + L::O_OFF + q * L::BLOCK + wq * 4096, lane, tm_o, q ? G.hq[1] : G.hq[0],
                     qt * BM + wq * 32, G.b, p.n_q);
     // O of this query tile has been read: the next unit's first P V may overwrite it
     // (ordered by this warpgroup's next p_full arrival).
@@ -594,7 +908,7 @@ __device__ void softmax_wg(const Params& p, uint8_t* smem, Bars* bars, uint32_t 
   }
 }
 
-template <int D>
+template <int D, bool I4, bool MOD>
 __global__ void __launch_bounds__(NTHREADS, 1)
     prefill_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tm_q,
                    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -645,17 +959,18 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   if (warp < 8) {
     // two softmax warpgroups take the registers the third one gives back
     asm volatile("setmaxnreg.inc.sync.aligned.u32 " HSWA_STR(HSWA_SOFTMAX_REGS) ";" ::: "memory");
-    softmax_wg<D>(p, smem, bars, tbase, warp >> 2, &tm_o);
+    softmax_wg<D, MOD>(p, smem, bars, tbase, warp >> 2, &tm_o);
     if ((threadIdx.x & 31) == 0) bulk_wait_all();  // output stores complete before the CTA exits
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 " HSWA_STR(HSWA_PRODUCER_REGS) ";" ::: "memory");
     if (warp == PRODUCER_WARP) {
-      producer<D>(p, smem, bars, &tm_q, &tm_k, &tm_v, &tm_rk, &tm_rv);
+      producer<D, I4, MOD>(p, smem, bars, &tm_q, &tm_k, &tm_v, &tm_rk, &tm_rv);
     } else if (warp == MMA_WARP) {
-      if ((threadIdx.x & 31) == 0) mma_issuer<D>(p, smem, bars, tbase);
+      if ((threadIdx.x & 31) == 0) mma_issuer<D, MOD>(p, smem, bars, tbase);
       __syncwarp();
     } else if (p.conv) {
-      if constexpr (D == 128) page_converter<D>(p, smem, bars);
+      if constexpr (I4) page_converter_i4<D, MOD>(p, smem, bars);
+      else if constexpr (D == 128) page_converter<D, MOD>(p, smem, bars);
     }
   }
 
@@ -672,7 +987,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 int launch_prefill(const PrefillLaunch& Lc, cudaStream_t stream) {
   // narrow windows: every query tile's band fits in two key tiles, which stay resident while
   // all query heads of a KV head pass through them
-  if (Lc.window >= 1 && Lc.window <= BN + 1) return launch_prefill_narrow(Lc, stream);
+  if (!Lc.mod && Lc.window >= 1 && Lc.window <= BN + 1) return launch_prefill_narrow(Lc, stream);
   const hswa_pool* pool = Lc.pool;
   const hswa_pool_desc& D = pool->desc;
   Params p{};
@@ -692,7 +1007,10 @@ int launch_prefill(const PrefillLaunch& Lc, cudaStream_t stream) {
   p.ring_k8 = pool->ring_k8;
   p.ring_v8 = pool->ring_v8;
   p.fp8 = pool->fp8 ? 1 : 0;
-  p.conv = (pool->fp8 && Lc.window == 0) ? 1 : 0;
+  p.conv = ((pool->fp8 || pool->i4) && Lc.window == 0) ? 1 : 0;
+  p.blk_bytes = Lc.window > 0 ? pool->ring_blk : pool->page_blk;
+  p.page_k8 = pool->page_k8;
+  p.page_v8 = pool->page_v8;
   if (pool->fp8) {
     const int n_layers = D.n_swa_layers + D.n_full_layers;
     p.k_scale = pool->scales + (size_t)(0 * n_layers + Lc.layer) * D.n_kv_heads;
@@ -727,19 +1045,42 @@ int launch_prefill(const PrefillLaunch& Lc, cudaStream_t stream) {
 
   const CUtensorMap& rk = pool->ring_tma ? pool->tm_ring_k : Lc.tm_k;
   const CUtensorMap& rv = pool->ring_tma ? pool->tm_ring_v : Lc.tm_v;
-  if (p.conv && Lc.d != 128) {
+  if (pool->fp8 && p.conv && Lc.d != 128) {
     set_error("prefill: FP8 pages are read with head_dim 128 only");
     return HSWA_ERR_UNSUPPORTED_SHAPE;
   }
-  if (Lc.d == 128) {
-    const int smem = Layout<128>::BYTES + 1024;
-    cudaFuncSetAttribute(prefill_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    prefill_kernel<128><<<grid, NTHREADS, smem, stream>>>(p, Lc.tm_q, Lc.tm_k, Lc.tm_v, rk, rv, Lc.tm_o);
-  } else {
-    const int smem = Layout<64>::BYTES + 1024;
-    cudaFuncSetAttribute(prefill_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    prefill_kernel<64><<<grid, NTHREADS, smem, stream>>>(p, Lc.tm_q, Lc.tm_k, Lc.tm_v, rk, rv, Lc.tm_o);
+  if (Lc.mod) {
+    fill_score_params(*Lc.mod, 1.0 / sqrt((double)Lc.d), &p.sp);
+    if (Lc.mod->key_begin || Lc.mod->key_end) {
+      int4* bounds = static_cast<int4*>(Lc.workspace);
+      int* order = reinterpret_cast<int*>(bounds + (size_t)Lc.B * p.n_tiles);
+      const int n = Lc.B * p.n_tiles;
+      bounds_kernel<<<(n + 7) / 8, 256, 0, stream>>>(p, bounds);
+      order_kernel<<<1, 1024, 0, stream>>>(p, bounds, order);
+      p.bounds = bounds;
+      p.order = order;
+    }
   }
+  const int smem = (Lc.d == 128 ? Layout<128>::BYTES : Layout<64>::BYTES) + 1024;
+#define HSWA_PREFILL(DD, I4_, MOD_)                                                                                 \
+  do {                                                                                                               \
+    cudaFuncSetAttribute(prefill_kernel<DD, I4_, MOD_>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);          \
+    prefill_kernel<DD, I4_, MOD_><<<grid, NTHREADS, smem, stream>>>(p, Lc.tm_q, Lc.tm_k, Lc.tm_v, rk, rv, Lc.tm_o);  \
+  } while (0)
+#define HSWA_PREFILL_D(DD)                                \
+  do {                                                    \
+    if (pool->i4) {                                       \
+      if (Lc.mod) HSWA_PREFILL(DD, true, true);           \
+      else HSWA_PREFILL(DD, true, false);                 \
+    } else {                                              \
+      if (Lc.mod) HSWA_PREFILL(DD, false, true);          \
+      else HSWA_PREFILL(DD, false, false);                \
+    }                                                     \
+  } while (0)
+  if (Lc.d == 128) HSWA_PREFILL_D(128);
+  else HSWA_PREFILL_D(64);
+#undef HSWA_PREFILL_D
+#undef HSWA_PREFILL
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {
     set_error("prefill: launch failed: %s", cudaGetErrorString(e));

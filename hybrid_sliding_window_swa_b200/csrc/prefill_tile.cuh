@@ -8,6 +8,7 @@
 // grows by more than 2^kTau, so P = 2^(s * scale * log2 e - m) stays below 2^kTau.
 #pragma once
 #include "common.cuh"
+#include "kv_quant.cuh"
 
 namespace hswa {
 namespace {
@@ -47,6 +48,98 @@ static_assert(2 * 128 * HSWA_SOFTMAX_REGS + 128 * HSWA_PRODUCER_REGS <= 384 * 16
 
 __device__ __forceinline__ constexpr bool use_poly(int pair) { return (pair & 7) >= 8 - HSWA_POLY_PER8; }
 
+// Modified scores of a call (hswa_score_mod), as a kernel takes them.
+struct ScoreParams {
+  float softcap;           // 0: none
+  float cap_in, cap_log2;  // 2 log2(e) scale / cap, cap log2 e
+  float poly_max;          // raw scores up to this magnitude take the polynomial (0: none do)
+  float poly[6];           // cap log2(e) tanh(x scale / cap) = x (poly[0] + poly[1] x^2 + ...)
+  const float* slope;      // [Hq] distance slopes, or null
+  const int64_t* key_begin;  // [B][n_q], or null
+  const int64_t* key_end;
+};
+
+inline void fill_score_params(const hswa_score_mod& m, double scale, ScoreParams* sp) {
+  *sp = ScoreParams{};
+  sp->softcap = m.softcap;
+  sp->slope = m.dist_slope;
+  sp->key_begin = m.key_begin;
+  sp->key_end = m.key_end;
+  if (m.softcap > 0.f) {
+    const double log2e = 1.4426950408889634, c1 = scale / (double)m.softcap;
+    sp->cap_in = (float)(2.0 * log2e * c1);
+    sp->cap_log2 = (float)(log2e * m.softcap);
+    // tanh(u) = u T(u^2) on |u| <= 1: interpolation at the 6 Chebyshev nodes of u^2 in [0, 1], off by at
+    // most 5e-7. The powers of u's factor are folded into the coefficients, for caps whose folded
+    // coefficients and powers stay well inside the fp32 range.
+    const double T[6] = {0.9999993948006503,  -0.33328951370216614, 0.1328072064598301,
+                         -0.05158598840417456, 0.01672085517953942, -0.0030582290375864097};
+    if (c1 >= 6e-4 && c1 <= 100.0) {
+      sp->poly_max = (float)(1.0 / c1);
+      double f = log2e * m.softcap * c1;
+      for (int i = 0; i < 6; ++i, f *= c1 * c1) sp->poly[i] = (float)(T[i] * f);
+    }
+  }
+}
+
+// The 128 raw scores of a row -> z log2(e), z = cap tanh(s / cap) - slope |i - j|. c_q: the query's own
+// column (its position minus the tile's), so column k is |c_q - k| away.
+// The cap costs what tanh costs: through exponential and reciprocal it is two more MUFU operations per
+// score, on the unit that the softmax itself loads most. While every score of the warp stays within the
+// cap (|s| <= cap, the usual case), the degree-11 polynomial on the FMA pipe replaces them: 7 packed
+// multiply-adds per pair.
+__device__ __forceinline__ void modify_scores(uint32_t (&v)[128], const ScoreParams& sp, float sl2, float slope2,
+                                              float c_q) {
+  if (sp.softcap > 0.f) {
+    float m0 = 0.f, m1 = 0.f, m2 = 0.f, m3 = 0.f;
+#pragma unroll
+    for (int k = 0; k < 128; k += 8) {
+      m0 = fmax3(m0, fabsf(__uint_as_float(v[k])), fabsf(__uint_as_float(v[k + 1])));
+      m1 = fmax3(m1, fabsf(__uint_as_float(v[k + 2])), fabsf(__uint_as_float(v[k + 3])));
+      m2 = fmax3(m2, fabsf(__uint_as_float(v[k + 4])), fabsf(__uint_as_float(v[k + 5])));
+      m3 = fmax3(m3, fabsf(__uint_as_float(v[k + 6])), fabsf(__uint_as_float(v[k + 7])));
+    }
+    if (__all_sync(0xffffffffu, fmaxf(fmax3(m0, m1, m2), m3) <= sp.poly_max)) {
+      uint64_t c[6];
+#pragma unroll
+      for (int i = 0; i < 6; ++i) c[i] = f2_pack(sp.poly[i], sp.poly[i]);
+#pragma unroll
+      for (int k = 0; k < 128; k += 2) {
+        const uint64_t x = f2_pack(__uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+        const uint64_t t = f2_mul(x, x);
+        uint64_t y = f2_fma(c[5], t, c[4]);
+        y = f2_fma(y, t, c[3]);
+        y = f2_fma(y, t, c[2]);
+        y = f2_fma(y, t, c[1]);
+        y = f2_fma(y, t, c[0]);
+        y = f2_mul(x, y);
+        float a, b;
+        f2_unpack(y, a, b);
+        v[k] = __float_as_uint(a);
+        v[k + 1] = __float_as_uint(b);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 128; ++k)
+        v[k] = __float_as_uint(capped_log2(__uint_as_float(v[k]), sp.cap_in, sp.cap_log2));
+    }
+  } else {
+    const uint64_t s2 = f2_pack(sl2, sl2);
+#pragma unroll
+    for (int k = 0; k < 128; k += 2) {
+      float a, b;
+      f2_unpack(f2_mul(f2_pack(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), s2), a, b);
+      v[k] = __float_as_uint(a);
+      v[k + 1] = __float_as_uint(b);
+    }
+  }
+  if (sp.slope) {
+#pragma unroll
+    for (int k = 0; k < 128; ++k)
+      v[k] = __float_as_uint(fmaf(-slope2, fabsf(c_q - (float)k), __uint_as_float(v[k])));
+  }
+}
+
 // One key tile of one query row. trow: this warp's TMEM lane base; S of the row in columns
 // [s_col, s_col + 128), O in [o_col, o_col + D). Columns outside [c_lo, c_hi] are masked when
 // `edge`. m_used / l: running maximum (log2 domain) and row sum; o_live: O already holds a
@@ -61,10 +154,14 @@ __device__ __forceinline__ constexpr bool use_poly(int pair) { return (pair & 7)
 //     chunk is wholly in or out for the whole warp. The warp loads chunk (w + c) & 3 into
 //     register block c (rot = w), masks block 0 by lane and selects the other blocks whole;
 //     `lower_edge` marks the tile before the diagonal. Single-pass softmax only.
-template <int D, int MASK_MODE>
+//
+// MOD: the scores are modified first (modify_scores) and come out in the log2 domain.
+template <int D, int MASK_MODE, bool MOD = false>
 __device__ __forceinline__ void softmax_tile(uint32_t trow, uint32_t s_col, uint32_t o_col, float sl2, bool edge,
                                              int c_lo, int c_hi, float& m_used, float& l, bool o_live,
-                                             int rot = 0, bool lower_edge = false) {
+                                             int rot = 0, bool lower_edge = false, const ScoreParams* sp = nullptr,
+                                             float slope2 = 0.f, float c_q = 0.f) {
+  static_assert(!MOD || HSWA_SOFTMAX_SINGLE_PASS, "modified scores need the single-pass softmax");
   static_assert(MASK_MODE != 2 || HSWA_SOFTMAX_SINGLE_PASS, "the rotated mask needs the single-pass softmax");
   constexpr bool BRANCH_FREE_MASK = MASK_MODE == 1;
   const int rc = MASK_MODE == 2 ? rot : 0;  // chunk rotation (0 folds away in the other modes)
@@ -80,6 +177,10 @@ __device__ __forceinline__ void softmax_tile(uint32_t trow, uint32_t s_col, uint
     reg_fence_into<32>(v);
     reg_fence_into<64>(v);
     reg_fence_into<96>(v);
+    if constexpr (MOD) {
+      modify_scores(v, *sp, sl2, slope2, c_q);
+      sl2 = 1.f;
+    }
     if (MASK_MODE == 2) {
       // block 0 = chunk rot: the lower edge keeps j > lane, the diagonal keeps j <= lane
       const int lane = threadIdx.x & 31;
@@ -300,10 +401,12 @@ __device__ __forceinline__ void softmax_tile(uint32_t trow, uint32_t s_col, uint
 // Epilogue of one query tile: O / l -> bf16, staged per warp (its 32 rows x 128 B, 128-byte
 // swizzle, 4 KB at `stage`) and written by one TMA store per 64-column half into the output
 // map at (column, head h, row0 .. row0 + 31, batch b); rows past n_q fall outside the map.
-template <int D>
+// MAY_BE_EMPTY: a row with l = 0 saw no key (its O columns may never have been written) and gives zeros.
+template <int D, bool MAY_BE_EMPTY = false>
 __device__ __forceinline__ void store_output(uint32_t trow, uint32_t o_col, float l, uint8_t* stage, int lane,
                                              const CUtensorMap* tm_o, int h, int row0, int b, int n_q) {
   const float inv = 1.f / l;
+  const bool none = MAY_BE_EMPTY && l == 0.f;
 #pragma unroll
   for (int dh = 0; dh < D / 64; ++dh) {
     if (lane == 0) bulk_wait_read_all();  // the previous store from this buffer has read it
@@ -318,6 +421,10 @@ __device__ __forceinline__ void store_output(uint32_t trow, uint32_t o_col, floa
 #pragma unroll
       for (int k = 0; k < 32; k += 2)
         pk[k >> 1] = pack_bf16x2(__uint_as_float(o[k]) * inv, __uint_as_float(o[k + 1]) * inv);
+      if (none) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) pk[k] = 0u;
+      }
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const int chunk = (c0 >> 3) + x;
@@ -462,6 +569,70 @@ __device__ __forceinline__ void ring_rows_fp8(const uint8_t* ring_rows, bool ok,
         const int blk = cc >> 3, ch = cc & 7;
         *reinterpret_cast<uint4*>(dst + blk * blk_stride + r * 128 + ((ch ^ (r & 7)) << 4)) =
             make_uint4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
+      }
+    }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// Eight 4-bit codes (a word) -> 16 bytes of bf16 values code * step + lo, dims in order. Each code is
+// planted in the mantissa of 128 (bf16 128 + code, exact), 128 is subtracted (exact) and one bf16x2
+// fused multiply-add rounds once.
+__device__ __forceinline__ uint4 i4x8_bf16(uint32_t w, __nv_bfloat162 step, __nv_bfloat162 lo) {
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t z = (w >> (8 * i)) & 0xFFu;
+    const uint32_t pair = ((z * 0x1001u) & 0x000F000Fu) | 0x43004300u;
+    const __nv_bfloat162 c = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&pair), __nv_bfloat162(128.f, 128.f));
+    const __nv_bfloat162 y = __hfma2(c, step, lo);
+    o[i] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+__device__ __forceinline__ void i4_pair_bf162(uint32_t pair, __nv_bfloat162& step, __nv_bfloat162& lo) {
+  const uint32_t s = __byte_perm(pair, pair, 0x1010), l = __byte_perm(pair, pair, 0x3232);
+  step = *reinterpret_cast<const __nv_bfloat162*>(&s);
+  lo = *reinterpret_cast<const __nv_bfloat162*>(&l);
+}
+
+// ring_rows_fp8 for a 4-bit ring block (W rows of codes, then the pairs).
+template <int D>
+__device__ __forceinline__ void ring_rows_i4(const uint8_t* block, bool ok, int held_lo, int held_hi, int W,
+                                             uint8_t* dst, int kb, int lane, int blk_stride = BM * 128) {
+  constexpr int CPR = D / 32;  // 16-byte chunks of codes per row
+  constexpr int TOTAL = BN * CPR;
+  constexpr int BATCH = 4;
+  static_assert(TOTAL % (32 * BATCH) == 0, "tile chunks");
+  const uint32_t* pairs = reinterpret_cast<const uint32_t*>(block + (int64_t)W * (D / 2));
+  for (int base = 0; base < TOTAL; base += 32 * BATCH) {
+    uint4 x[BATCH];
+    uint32_t pr[BATCH];
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) {
+      const int idx = base + u * 32 + lane;
+      const int r = idx / CPR, c = idx % CPR;
+      const int pos = kb + r;
+      const bool held = ok && pos >= held_lo && pos < held_hi;
+      const int slot = held ? pos % W : 0;
+      x[u] = held ? __ldg(reinterpret_cast<const uint4*>(block + (int64_t)slot * (D / 2) + c * 16))
+                  : make_uint4(0, 0, 0, 0);
+      pr[u] = held ? __ldg(pairs + slot) : 0u;
+    }
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) {
+      const int idx = base + u * 32 + lane;
+      const int r = idx / CPR, c = idx % CPR;
+      const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+      __nv_bfloat162 step, lo;
+      i4_pair_bf162(pr[u], step, lo);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int cc = 4 * c + i;  // 16-byte chunk of the row in bf16
+        *reinterpret_cast<uint4*>(dst + (cc >> 3) * blk_stride + r * 128 + (((cc & 7) ^ (r & 7)) << 4)) =
+            i4x8_bf16(w[i], step, lo);
       }
     }
   }

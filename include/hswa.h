@@ -210,16 +210,17 @@ HSWA_API int kv_pool_gather_ring(hswa_pool* pool, int layer, int32_t dst_seq, co
  * the chunk with kv_pool_append afterwards. Key tiles wholly outside every
  * query's window are skipped, not masked. fp32 accumulation and softmax.
  * W = 1: the window is the diagonal alone, so o_i = v_i of the query head's KV head; the call
- * copies those rows (q, k and the ring are not read). FP8 pools: keys before start_pos come from
- * the ring dequantized (code value times scale, rounded to bf16); the chunk's own k and v are
- * used as given. */
+ * copies those rows (q, k and the ring are not read). FP8 and 4-bit pools: keys before start_pos
+ * come from the ring dequantized and rounded to bf16 (FP8: code value times scale); the chunk's own
+ * k and v are used as given. */
 HSWA_API int swa_prefill_fwd(hswa_pool* pool, int layer, const hswa_bf16* q, const hswa_bf16* k,
                     const hswa_bf16* v, hswa_bf16* o, int B, int n_q, const int64_t* start_pos,
                     const int32_t* seq_ids, int n_q_heads, void* stream);
 
 /* Full causal attention for one chunk of n_q tokens per sequence over the paged
  * pool of full layer `layer`: query i = start_pos[b] + t attends positions 0..i,
- * all read through the page table (the chunk itself must already be appended).
+ * all read through the page table (the chunk itself must already be appended). FP8 and 4-bit entries
+ * are read dequantized and rounded to bf16.
  *  q, o      [B][n_q][n_q_heads][head_dim] bf16
  *  start_pos device int64[B] (NULL for 0); page_table device int32[B][pt_stride]. */
 HSWA_API int full_prefill_fwd(hswa_pool* pool, int layer, const hswa_bf16* q, hswa_bf16* o, int B,
@@ -266,14 +267,28 @@ HSWA_API int hybrid_decode_fwd(hswa_pool* pool, int layer, const hswa_bf16* q, c
  * or of the new tokens (decode: ctx_len + n_q_per_seq). So packed documents pass the first position of
  * the query's document as key_begin; a prefix (or image) seen in both directions passes its end as
  * key_end; a padded row passes key_end <= key_begin. A query that sees no key gives zeros.
- * What a query does not see changes nothing in its row whatever its keys hold; its values must be
- * finite (entries no query of the call sees may hold anything). */
+ * Keys a query does not see change nothing in its row, whatever they hold. Values must be finite between
+ * the smallest and the largest position the queries of a sequence see; outside it they may hold anything,
+ * and pages of such positions are not read. */
 typedef struct hswa_score_mod {
   float softcap;             /* 0: none; else finite and > 0 */
   const float* dist_slope;   /* device float32[n_q_heads], finite; NULL: none */
   const int64_t* key_begin;  /* device int64[B][n_q], any values; NULL: 0 */
   const int64_t* key_end;    /* device int64[B][n_q], any values; NULL: i + 1 */
 } hswa_score_mod;
+
+/* swa_prefill_fwd and full_prefill_fwd with modified scores; key_begin and key_end are [B][n_q]. With
+ * either of them, `workspace` holds at least prefill_mod_workspace_size() bytes, 256-byte aligned, whose
+ * contents on entry do not matter; calls sharing one workspace must not overlap. Without them it may be
+ * NULL. Tiles of the (query, key) plane in which no query sees a key are neither read nor computed. */
+HSWA_API int prefill_mod_workspace_size(const hswa_pool* pool, int B, int n_q, size_t* bytes);
+HSWA_API int swa_prefill_mod_fwd(hswa_pool* pool, int layer, const hswa_bf16* q, const hswa_bf16* k,
+                                 const hswa_bf16* v, hswa_bf16* o, int B, int n_q, const int64_t* start_pos,
+                                 const int32_t* seq_ids, int n_q_heads, const hswa_score_mod* mod, void* workspace,
+                                 size_t ws_bytes, void* stream);
+HSWA_API int full_prefill_mod_fwd(hswa_pool* pool, int layer, const hswa_bf16* q, hswa_bf16* o, int B, int n_q,
+                                  const int64_t* start_pos, const int32_t* page_table, int pt_stride, int n_q_heads,
+                                  const hswa_score_mod* mod, void* workspace, size_t ws_bytes, void* stream);
 
 /* hybrid_decode_fwd with modified scores. key_begin and key_end are [n_seqs][n_q_per_seq]. Same
  * workspace (hybrid_decode_workspace_size) and supported pools. */
