@@ -822,7 +822,7 @@ __device__ void mma_issuer(const Params& p, uint8_t* smem, Bars* bars, uint32_t 
       umma_commit(&bars->v_empty[prev_s]);
     }
     for (int q = 0; q < NQT; ++q)
-      if (G.act[q]) umma_commit(&bars->o_full[q]);
+      if (G.act[q] && (!MOD || G.jhi[q] >= G.jlo[q])) umma_commit(&bars->o_full[q]);
   }
 }
 
@@ -897,8 +897,12 @@ __device__ void softmax_wg(const Params& p, uint8_t* smem, Bars* bars, uint32_t 
       ++n_done;
     }
 
-    if (!mbar_wait(&bars->o_full[q], no & 1, p.err)) return;
-    ++no;
+    // (a tile in which no row sees a key has no products: nothing would hold the issuer back from
+    // completing o_full again for a later unit, so neither side uses it there)
+    if (!MOD || qjhi >= qjlo) {
+      if (!mbar_wait(&bars->o_full[q], no & 1, p.err)) return;
+      ++no;
+    }
     tc_fence_after();
     store_output<D, MOD>(trow, o_col, l, smem + L::O_OFF + q * L::BLOCK + wq * 4096, lane, tm_o, q ? G.hq[1] : G.hq[0],
                     qt * BM + wq * 32, G.b, p.n_q);

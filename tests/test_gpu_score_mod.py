@@ -259,6 +259,27 @@ def test_plain_mod_equals_plain_call_within_rounding_and_repeats_bit_for_bit():
     assert torch.equal(c[0], c[1]) and torch.equal(c[0], c[2])
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 128), (3, 1, 64)])
+@pytest.mark.parametrize("which", ["tail", "all", "every_other_tile"])
+def test_tiles_that_see_nothing(hq, hkv, d, which):
+    # many units in a row without a single key
+    n, B = 1500, 3
+    pool = make_pool(BF, hkv, d, 0, 1, 64, B, 24 * B)
+    pt = torch.arange(24 * B, dtype=torch.int32).view(B, 24).cuda()
+    k, v, q = randn(1, B, n, hkv, d), randn(2, B, n, hkv, d), randn(3, B, n, hq, d)
+    hs.kv_pool_append(pool, 0, k.cuda(), v.cuda(), torch.zeros(B, dtype=torch.int64).cuda(), page_table=pt)
+    i = torch.arange(n)
+    empty = {"tail": i >= 300, "all": i >= 0, "every_other_tile": (i // 128) % 2 == 0}[which]
+    end = torch.where(empty, torch.zeros_like(i), i + 1)[None].expand(B, n).contiguous()
+    ws = torch.empty(hs.prefill_mod_workspace_size(pool, B, n), dtype=torch.uint8, device="cuda")
+    o = hs.full_prefill_mod_fwd(pool, 0, q.cuda(), pt, hs.ScoreMod(key_end=end.cuda()), ws)
+    assert hs.hswa_pool_check_error(pool) == 0
+    assert (o[:, empty.cuda()] == 0).all()
+    lo, hi = ref.ranges(n, 0, n, 0, None, end[0])
+    for b in range(B):
+        ref.check(o[b], ref.attention(q[b], k[b], v[b], lo, hi), f"seq {b}")
+
+
 def test_rows_past_the_chunk_are_left_as_they_were():
     hq, hkv, d, n = 2, 1, 64, 130
     pool = make_pool(BF, hkv, d, 0, 1, 64, 1, 4)
