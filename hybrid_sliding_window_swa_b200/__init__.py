@@ -9,6 +9,7 @@ or a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from dataclasses import dataclass
 
@@ -142,12 +143,19 @@ def _ptr(t: torch.Tensor | None, dtype=None, name: str = "tensor"):
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
+
+
+# The current stream's handle without building a Stream object (3.5 us a call, more than a small kernel).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 @dataclass(frozen=True)
@@ -298,7 +306,8 @@ class RopeDesc:
     n_axes: int = 1
     interleaved: bool = False
 
-    def c(self) -> RopeDescC:
+    def c(self):
+        """Pointer to the C descriptor (built once)."""
         c = self.__dict__.get("_c")
         if c is None:
             n = len(self.inv_freq)
@@ -307,7 +316,8 @@ class RopeDesc:
                 raise ValueError("one axis per frequency, at most 64 frequencies")
             c = RopeDescC(2 * n, self.n_axes, int(self.interleaved), 0, (ctypes.c_double * 64)(*map(float, self.inv_freq)),
                           (ctypes.c_uint8 * 64)(*map(int, axis)))
-            object.__setattr__(self, "_c", c)
+            object.__setattr__(self, "_c", ctypes.pointer(c))
+            c = self.__dict__["_c"]
         return c
 
 
@@ -334,19 +344,25 @@ def rope_fwd(rope: RopeDesc, q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor
              k_out: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """Rotate q [..., Hq, d] and k [..., Hkv, d] of the same tokens by their positions pos
     [n_axes, tokens] (int64). q_out / k_out may be q / k."""
-    n = q.numel() // (q.shape[-1] * q.shape[-2]) if q.numel() else 0
-    if q.shape[:-2] != k.shape[:-2] or q.shape[-1] != k.shape[-1]:
+    qs, ks = q.shape, k.shape
+    d = qs[-1]
+    if qs[:-2] != ks[:-2] or d != ks[-1]:
         raise ValueError("q and k must have the same tokens and head_dim")
+    n = math.prod(qs[:-2])
     if pos.shape[0] != rope.n_axes or pos.numel() != rope.n_axes * n:
         raise ValueError(f"pos must be [n_axes, tokens] = [{rope.n_axes}, {n}], got {tuple(pos.shape)}")
-    q_out = torch.empty_like(q) if q_out is None else q_out
-    k_out = torch.empty_like(k) if k_out is None else k_out
-    if q_out.shape != q.shape or k_out.shape != k.shape:
-        raise ValueError("q_out and k_out must have the shapes of q and k")
+    if q_out is None:
+        q_out = torch.empty_like(q)
+    elif q_out.shape != qs:
+        raise ValueError("q_out must have the shape of q")
+    if k_out is None:
+        k_out = torch.empty_like(k)
+    elif k_out.shape != ks:
+        raise ValueError("k_out must have the shape of k")
     _check(load_library().rope_fwd(
-        ctypes.byref(rope.c()), q.shape[-1], n, _ptr(pos, torch.int64, "pos"), _ptr(q, torch.bfloat16, "q"),
-        _ptr(q_out, torch.bfloat16, "q_out"), q.shape[-2], _ptr(k, torch.bfloat16, "k"),
-        _ptr(k_out, torch.bfloat16, "k_out"), k.shape[-2], _stream(stream)))
+        rope.c(), d, n, _ptr(pos, torch.int64, "pos"), _ptr(q, torch.bfloat16, "q"),
+        _ptr(q_out, torch.bfloat16, "q_out"), qs[-2], _ptr(k, torch.bfloat16, "k"),
+        _ptr(k_out, torch.bfloat16, "k_out"), ks[-2], _stream(stream)))
     return q_out, k_out
 
 
@@ -369,7 +385,7 @@ def kv_pool_append_rope(pool: KVPool, layer: int, rope: RopeDesc, q: torch.Tenso
         k_out = torch.empty_like(k)
     pt_stride = page_table.shape[1] if page_table is not None else 0
     _check(load_library().kv_pool_append_rope(
-        pool.handle, layer, ctypes.byref(rope.c()), _ptr(pos, torch.int64, "pos"), n_seqs,
+        pool.handle, layer, rope.c(), _ptr(pos, torch.int64, "pos"), n_seqs,
         _ptr(seq_ids, torch.int32, "seq_ids"), _ptr(start_pos, torch.int64, "start_pos"), n_tok,
         _ptr(q, torch.bfloat16, "q"), _ptr(q_out, torch.bfloat16, "q_out"), q.shape[2], _ptr(k, torch.bfloat16, "k"),
         _ptr(k_out, torch.bfloat16, "k_out"), _ptr(v, torch.bfloat16, "v"),

@@ -115,6 +115,7 @@ struct DecParams {
   int* err;
   // extended launches (4-bit pools, score modifications)
   int split;               // cached keys per split
+  int small;               // at most 32 sequences: no plan kernel (SmallPlan)
   int64_t blk_bytes;       // bytes of a ring block
   float scale_nat;         // softmax scale without log2 e
   float softcap, cap_in, cap_log2;
@@ -214,6 +215,11 @@ __device__ __forceinline__ int class_b(const DecParams& p, int s, int64_t L) {
   return c < NCLS_B - 1 ? c : NCLS_B - 1;
 }
 
+// Programmatic dependent launch: the launch may begin before its predecessor in the stream has finished;
+// grid_wait holds until that has, with its writes visible. grid_go lets the successor begin.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Builds the work list (see PlanView) and resets the work counter. One block of 1024 threads:
 // class totals, then a stable placement chunk by chunk (warp ballots give each thread its rank
 // among earlier threads of its class), then prefix sums of the body splits in part-A order.
@@ -229,6 +235,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(DecParams p) {
   __shared__ int warp_sums[32];
   __shared__ int carry;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  if constexpr (EXT) grid_go();
   if (tid < NC) cnt[tid] = 0;
   __syncthreads();
   for (int base = 0; base < p.n_seqs; base += 1024) {
@@ -1004,13 +1011,13 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) decode_kernel(DecParams p) {
 //           (shuffles within the 8-thread group), keeping the factors 2^(m_c - M) in shared memory;
 //  phase 2: each thread owns 4 float4 groups of the R x D output and walks the splits with
 //           8 independent loads in flight.
-template <int D, bool EXT>
+template <int D>
 __global__ void __launch_bounds__(256) merge_kernel(DecParams p) {
   const int g = blockIdx.x % p.Hkv;
   const int s = blockIdx.x / p.Hkv;
   const WsHeader* hdr = reinterpret_cast<const WsHeader*>(p.ws);
   const PlanView pv(p.ws, p.n_seqs);
-  const int nsp = n_splits_x<EXT>(p, s, safe_len(p, s));
+  const int nsp = n_splits(p, safe_len(p, s));
   if (nsp <= 1) return;
   extern __shared__ float msh[];  // [nsp][R] scale factors, then [R] inverse denominators
   float* fac = msh;
@@ -1044,7 +1051,7 @@ __global__ void __launch_bounds__(256) merge_kernel(DecParams p) {
     den += __shfl_xor_sync(0xffffffffu, den, 1);
     den += __shfl_xor_sync(0xffffffffu, den, 2);
     den += __shfl_xor_sync(0xffffffffu, den, 4);
-    if (live && lane8 == 0) inv[r] = EXT && den == 0.f ? 0.f : 1.f / den;
+    if (live && lane8 == 0) inv[r] = 1.f / den;
   }
   __syncthreads();
   constexpr int Q4 = D / 4;  // float4 groups per row
@@ -1107,6 +1114,154 @@ __global__ void __launch_bounds__(256) merge_kernel(DecParams p) {
   }
 }
 
+// Up to 32 sequences: no plan kernel. Every warp that needs the work list works it out itself, one lane per
+// sequence: the splits before the last one ("body"), their exclusive prefix sums in sequence order, and the
+// total; items are the body splits in sequence order, then the last splits. CTAs take items in strides of
+// the grid. (One launch and its ~5 us chain of block barriers less, which is most of a short call.)
+struct SmallPlan {
+  int L, body, excl, total;  // L, body, excl: this lane's sequence
+  __device__ __forceinline__ explicit SmallPlan(const DecParams& p) {
+    const int lane = threadIdx.x & 31;
+    L = lane < p.n_seqs ? (int)safe_len(p, lane) : 0;
+    body = lane < p.n_seqs ? n_splits_x<true>(p, lane, L) - 1 : 0;
+    int x = body;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
+    }
+    excl = x - body;
+    total = __shfl_sync(0xffffffffu, x, 31);
+  }
+};
+
+// The split merge of the extended launches: WPR warps per (sequence, query head row), so that a few long
+// sequences still spread over many SMs and every partial of a row is in flight at once: merge_kernel's one
+// CTA per (sequence, KV head) took 20 us of a 119 us call for one 256K-token sequence, and one warp per row
+// walking 74 splits 15 us. A warp takes every WPR-th split, 8 at a time (maxima, sums and its lanes' columns
+// in one round trip), and the warps' states meet in shared memory.
+template <int D, int WPR>
+__global__ void __launch_bounds__(WPR == 1 ? 128 : WPR * 32) merge_rows_kernel(DecParams p) {
+  constexpr int V = D / 32;  // columns per lane
+  __shared__ float sh_m[WPR], sh_l[WPR], sh_o[WPR][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row = WPR == 1 ? (int64_t)blockIdx.x * 4 + warp : (int64_t)blockIdx.x;
+  const bool live = row < (int64_t)p.n_seqs * p.Hkv * p.R;
+  const int r = live ? (int)(row % p.R) : 0;
+  const int64_t sg = live ? row / p.R : 0;
+  const int g = (int)(sg % p.Hkv), s = (int)(sg / p.Hkv);
+  int body, first, last;  // splits before the last one, and where both kinds start in the work list
+  if (p.small) {
+    const SmallPlan sp(p);  // lengths and ranges are inputs: no need to wait for the decode kernel
+    body = __shfl_sync(0xffffffffu, sp.body, s);
+    first = __shfl_sync(0xffffffffu, sp.excl, s);
+    last = sp.total + s;
+    grid_wait();
+  } else {
+    grid_wait();
+    const WsHeader* hdr = reinterpret_cast<const WsHeader*>(p.ws);
+    const PlanView pv(p.ws, p.n_seqs);
+    const int pa = pv.inv_a[s];
+    first = pv.prefix[pa];
+    body = pv.prefix[pa + 1] - first;
+    last = hdr->body_total + pv.inv_b[s];
+  }
+  if (!live || body == 0) return;  // (every thread has waited: this grid ends after the decode kernel)
+  const int nsp = body + 1;
+  auto part = [&](int c) -> const float* {
+    const int64_t item = (int64_t)(c < body ? first + c : last) * p.Hkv + g;
+    return reinterpret_cast<const float*>(p.ws + p.part_off + (size_t)item * p.part_bytes);
+  };
+  float M = -INFINITY, den = 0.f, acc[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = 0.f;
+  for (int c0 = WPR == 1 ? 0 : warp; c0 < nsp; c0 += 8 * WPR) {
+    float m[8], l[8], y[8][V];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int c = c0 + k * WPR;
+      const float* q = part(c < nsp ? c : nsp - 1);
+      m[k] = c < nsp ? q[p.R * D + r] : -INFINITY;
+      l[k] = q[p.R * D + p.R + r];
+      if constexpr (V == 4) {
+        const float4 t = *reinterpret_cast<const float4*>(q + r * D + lane * 4);
+        y[k][0] = t.x; y[k][1] = t.y; y[k][2] = t.z; y[k][3] = t.w;
+      } else {
+        const float2 t = *reinterpret_cast<const float2*>(q + r * D + lane * 2);
+        y[k][0] = t.x; y[k][1] = t.y;
+      }
+    }
+    float mn = M;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) mn = fmaxf(mn, m[k]);
+    if (mn == -INFINITY) continue;  // nothing seen so far
+    const float al = ex2_approx(M - mn);
+    M = mn;
+    den *= al;
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] *= al;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float f = ex2_approx(m[k] - M);
+      if (m[k] == -INFINITY) continue;  // an empty split's columns are not read
+      den = fmaf(f, l[k], den);
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] = fmaf(f, y[k][v], acc[v]);
+    }
+  }
+  if constexpr (WPR > 1) {
+    if (lane == 0) {
+      sh_m[warp] = M;
+      sh_l[warp] = den;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) sh_o[warp][lane * V + v] = acc[v];
+    __syncthreads();
+    if (warp != 0) return;
+    float mn = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) mn = fmaxf(mn, sh_m[w]);
+    den = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = 0.f;
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) {
+      const float f = mn == -INFINITY ? 0.f : ex2_approx(sh_m[w] - mn);
+      den = fmaf(f, sh_l[w], den);
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] = fmaf(f, sh_o[w][lane * V + v], acc[v]);
+    }
+  }
+  const float iv = den == 0.f ? 0.f : 1.f / den;  // a row that sees nothing gives zeros
+  const int t = r / p.G, hh = r % p.G;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (((int64_t)s * p.n_qt + t) * p.Hq + g * p.G + hh) * D + lane * V);
+#pragma unroll
+  for (int v = 0; v < V; v += 2) dst[v / 2] = pack_bf16x2(acc[v] * iv, acc[v + 1] * iv);
+}
+
+// Launch with programmatic dependence on the launch before it in the stream.
+template <typename K>
+cudaError_t launch_dependent(K kernel, int grid, int block, size_t smem, cudaStream_t stream, const DecParams& p) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <int D>
+cudaError_t launch_merge_rows(const DecParams& p, int64_t max_splits, cudaStream_t stream) {
+  const int64_t rows = (int64_t)p.n_seqs * p.Hkv * p.R;
+  if (max_splits > 8) return launch_dependent(merge_rows_kernel<D, 8>, (int)rows, 256, 0, stream, p);
+  return launch_dependent(merge_rows_kernel<D, 1>, (int)((rows + 3) / 4), 128, 0, stream, p);
+}
+
 #include "decode_tc.cuh"
 #include "decode_i4.cuh"
 
@@ -1117,21 +1272,28 @@ int64_t max_splits(int window, int64_t max_ctx_len, int split = SPLIT) {
   return nsp < 1 ? 1 : nsp;
 }
 
-// Keys per split of an extended launch. Long enough that the merge is small against the reads (8192, as
-// in the other launches), shorter when the sequences would not fill the CTAs otherwise: about
-// kSplitItems work items over all (sequence, KV head) pairs if every context has the maximum length.
-constexpr int64_t kSplitItems = 592;  // two items for each of 148 x 2 resident CTAs
+// Keys per split of an extended launch, from the sizes the host knows. One sequence: as many equal splits as
+// fill the resident CTAs once (a second round would pay the start and the merge of an item again: 104 us
+// against 89 us for 256K tokens). Several sequences, whose lengths may differ: about four items per CTA if
+// all were of the largest length, but at least 2048 keys (an item costs some 4 us besides its reads) unless
+// one round would not be full. At most 8192 keys, as in the other launches.
+constexpr int64_t kExtCtas = 296;  // two CTAs on each of 148 SMs
 int ext_split(int n_seqs, int Hkv, int window, int64_t max_ctx_len) {
   const int64_t cached = window > 0 && max_ctx_len > window ? window : max_ctx_len;
-  const int64_t pairs = (int64_t)n_seqs * Hkv;
-  const int64_t want = pairs > 0 ? (kSplitItems + pairs - 1) / pairs : 1;
-  int64_t split = (cached + want - 1) / want;
+  const int64_t pairs = (int64_t)n_seqs * Hkv > 0 ? (int64_t)n_seqs * Hkv : 1;
+  auto cut = [&](int64_t n) { return (cached + n - 1) / n; };
+  int64_t split = cut(kExtCtas / pairs > 1 ? kExtCtas / pairs : 1);
+  if (n_seqs > 1) {
+    const int64_t fine = cut((4 * kExtCtas + pairs - 1) / pairs);
+    const int64_t least = split < 2048 ? split : 2048;
+    split = fine > least ? fine : least;
+  }
   split = (split + 63) / 64 * 64;
   return (int)(split < 256 ? 256 : (split > SPLIT ? SPLIT : split));
 }
 
 template <int D, int MT, bool FP8, bool EXT>
-int launch_t(DecParams& p, int n_items_max, int sms, size_t merge_smem, cudaStream_t stream) {
+int launch_t(DecParams& p, int n_items_max, int sms, int64_t nsp_max, size_t merge_smem, cudaStream_t stream) {
   using SM = DecSmem<D, MT, FP8>;
   plan_kernel<EXT><<<1, 1024, 0, stream>>>(p);
   cudaFuncSetAttribute(decode_kernel<D, MT, FP8, EXT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::BYTES);
@@ -1140,12 +1302,15 @@ int launch_t(DecParams& p, int n_items_max, int sms, size_t merge_smem, cudaStre
   if (grid > n_items_max) grid = n_items_max;
   if (grid < 1) grid = 1;
   decode_kernel<D, MT, FP8, EXT><<<grid, DEC_THREADS, SM::BYTES, stream>>>(p);
-  if (merge_smem > 0) {
+  cudaError_t e = cudaSuccess;
+  if constexpr (EXT) {
+    if (nsp_max > 1) e = launch_merge_rows<D>(p, nsp_max, stream);
+  } else if (nsp_max > 1) {
     if (merge_smem > 48 * 1024)
-      cudaFuncSetAttribute(merge_kernel<D, EXT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)merge_smem);
-    merge_kernel<D, EXT><<<p.n_seqs * p.Hkv, 256, merge_smem, stream>>>(p);
+      cudaFuncSetAttribute(merge_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)merge_smem);
+    merge_kernel<D><<<p.n_seqs * p.Hkv, 256, merge_smem, stream>>>(p);
   }
-  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) {
     set_error("hybrid_decode_fwd: launch failed: %s", cudaGetErrorString(e));
     return HSWA_ERR_CUDA;
@@ -1154,20 +1319,22 @@ int launch_t(DecParams& p, int n_items_max, int sms, size_t merge_smem, cudaStre
 }
 
 template <int D, int NT, int RG, bool MOD>
-int launch_i4(DecParams& p, int n_items_max, int sms, size_t merge_smem, cudaStream_t stream) {
+int launch_i4(DecParams& p, int n_items_max, int sms, int device, int64_t nsp_max, cudaStream_t stream) {
   using SM = I4Smem<D, NT, RG>;
-  plan_kernel<true><<<1, 1024, 0, stream>>>(p);
-  cudaFuncSetAttribute(decode_i4_kernel<D, NT, RG, MOD>, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::BYTES);
-  int grid = sms * 2;
+  HSWA_SET_SMEM((decode_i4_kernel<D, NT, RG, MOD>), SM::BYTES, device);
+  int grid = sms * I4_CTAS;
   if (grid > n_items_max) grid = n_items_max;
   if (grid < 1) grid = 1;
-  decode_i4_kernel<D, NT, RG, MOD><<<grid, I4_THREADS, SM::BYTES, stream>>>(p);
-  if (merge_smem > 0) {
-    if (merge_smem > 48 * 1024)
-      cudaFuncSetAttribute(merge_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)merge_smem);
-    merge_kernel<D, true><<<p.n_seqs * p.Hkv, 256, merge_smem, stream>>>(p);
+  p.small = p.n_seqs <= 32 ? 1 : 0;
+  cudaError_t e = cudaSuccess;
+  if (p.small) {
+    decode_i4_kernel<D, NT, RG, MOD><<<grid, I4_THREADS, SM::BYTES, stream>>>(p);
+  } else {
+    plan_kernel<true><<<1, 1024, 0, stream>>>(p);
+    e = launch_dependent(decode_i4_kernel<D, NT, RG, MOD>, grid, I4_THREADS, SM::BYTES, stream, p);
   }
-  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess && nsp_max > 1) e = launch_merge_rows<D>(p, nsp_max, stream);
+  if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) {
     set_error("hybrid_decode_fwd: launch failed: %s", cudaGetErrorString(e));
     return HSWA_ERR_CUDA;
@@ -1184,8 +1351,8 @@ int launch_tc(DecParams& p, int n_items_max, int sms, size_t merge_smem, cudaStr
   decode_tc_kernel<<<grid, TC_THREADS, smem, stream>>>(p);
   if (merge_smem > 0) {
     if (merge_smem > 48 * 1024)
-      cudaFuncSetAttribute(merge_kernel<128, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)merge_smem);
-    merge_kernel<128, false><<<p.n_seqs * p.Hkv, 256, merge_smem, stream>>>(p);
+      cudaFuncSetAttribute(merge_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)merge_smem);
+    merge_kernel<128><<<p.n_seqs * p.Hkv, 256, merge_smem, stream>>>(p);
   }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {
@@ -1197,6 +1364,11 @@ int launch_tc(DecParams& p, int n_items_max, int sms, size_t merge_smem, cudaStr
 
 }  // namespace
 
+int64_t decode_max_items(int n_seqs, int Hkv, int window, int64_t max_ctx_len, bool ext) {
+  const int split = ext ? ext_split(n_seqs, Hkv, window, max_ctx_len) : SPLIT;
+  return (int64_t)n_seqs * Hkv * max_splits(window, max_ctx_len, split);
+}
+
 size_t decode_workspace_bytes(int n_seqs, int n_qt, int Hq, int Hkv, int d, int window, int64_t max_ctx_len,
                               bool ext) {
   const int G = Hq / Hkv;
@@ -1206,8 +1378,9 @@ size_t decode_workspace_bytes(int n_seqs, int n_qt, int Hq, int Hkv, int d, int 
   return L.bytes;
 }
 
-size_t decode_merge_smem_bytes(int n_seqs, int n_qt, int Hq, int Hkv, int window, int64_t max_ctx_len, bool ext) {
-  const int64_t nsp = max_splits(window, max_ctx_len, ext ? ext_split(n_seqs, Hkv, window, max_ctx_len) : SPLIT);
+size_t decode_merge_smem_bytes(int n_seqs, int n_qt, int Hq, int Hkv, int window, int64_t max_ctx_len) {
+  (void)n_seqs;
+  const int64_t nsp = max_splits(window, max_ctx_len);
   if (nsp <= 1) return 0;
   // [nsp][R] scale factors and [R] inverse denominators
   return (size_t)(nsp + 1) * (size_t)(n_qt * (Hq / Hkv)) * sizeof(float);
@@ -1275,19 +1448,20 @@ int launch_decode(const DecodeLaunch& Lc, cudaStream_t stream) {
     return HSWA_ERR_UNSUPPORTED_SHAPE;
   }
   const int nmax = mi > 0x7fffffff ? 0x7fffffff : (int)mi;
-  const size_t msm = decode_merge_smem_bytes(p.n_seqs, p.n_qt, p.Hq, p.Hkv, p.window, p.max_ctx_len, Lc.ext);
+  const int64_t nsp_max = max_splits(p.window, p.max_ctx_len, p.split);
+  const size_t msm = decode_merge_smem_bytes(p.n_seqs, p.n_qt, p.Hq, p.Hkv, p.window, p.max_ctx_len);
   const int sms = pool->sms;
   if (pool->i4) {
 #define HSWA_I4(DD, MODD)                                                              \
-  (p.R <= 8    ? launch_i4<DD, 1, 1, MODD>(p, nmax, sms, msm, stream)                  \
-   : p.R <= 16 ? launch_i4<DD, 2, 1, MODD>(p, nmax, sms, msm, stream)                  \
-               : launch_i4<DD, 2, 2, MODD>(p, nmax, sms, msm, stream))
+  (p.R <= 8    ? launch_i4<DD, 1, 1, MODD>(p, nmax, sms, pool->device, nsp_max, stream)  \
+   : p.R <= 16 ? launch_i4<DD, 2, 1, MODD>(p, nmax, sms, pool->device, nsp_max, stream)  \
+               : launch_i4<DD, 2, 2, MODD>(p, nmax, sms, pool->device, nsp_max, stream))
     if (Lc.d == 128) return Lc.mod ? HSWA_I4(128, true) : HSWA_I4(128, false);
     return Lc.mod ? HSWA_I4(64, true) : HSWA_I4(64, false);
 #undef HSWA_I4
   }
   if (Lc.mod) {
-#define HSWA_DEC(DD, MM, F8) launch_t<DD, MM, F8, true>(p, nmax, sms, msm, stream)
+#define HSWA_DEC(DD, MM, F8) launch_t<DD, MM, F8, true>(p, nmax, sms, nsp_max, msm, stream)
     if (pool->fp8) {
       if (Lc.d == 128) return p.R <= 16 ? HSWA_DEC(128, 1, true) : HSWA_DEC(128, 2, true);
       return p.R <= 16 ? HSWA_DEC(64, 1, true) : HSWA_DEC(64, 2, true);
@@ -1305,7 +1479,7 @@ int launch_decode(const DecodeLaunch& Lc, cudaStream_t stream) {
   }();
   if (pool->fp8 && Lc.d == 128 && (tc_mode >= 2 || (tc_mode == 1 && p.window <= 0)))
     return launch_tc(p, nmax, sms, msm, stream);
-#define HSWA_DEC(DD, MM, F8) launch_t<DD, MM, F8, false>(p, nmax, sms, msm, stream)
+#define HSWA_DEC(DD, MM, F8) launch_t<DD, MM, F8, false>(p, nmax, sms, nsp_max, msm, stream)
   if (pool->fp8) {
     if (Lc.d == 128) return p.R <= 16 ? HSWA_DEC(128, 1, true) : HSWA_DEC(128, 2, true);
     return p.R <= 16 ? HSWA_DEC(64, 1, true) : HSWA_DEC(64, 2, true);

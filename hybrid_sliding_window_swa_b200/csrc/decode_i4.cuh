@@ -15,10 +15,11 @@
 // nothing. The codes go from shared memory to A fragments as they lie:
 //   K  lane (g, t) reads 16 bytes (D = 128) of key pi(g): 32 dims, whose order inside the dot product
 //      is free as long as Q is staged in the same order;
-//   V  lane (g, t) reads the bytes of its 16 dims (16 g ..) of keys t, 4 + t, 8 + t, 12 + t; two keys'
-//      words are interleaved by a byte permute, then masked. pi (the order of the 16 keys along S^T's
-//      rows) is chosen so that these are the keys 2t, 2t+1, 2t+8, 2t+9 of the P^T fragment, and both
-//      reads are free of bank conflicts.
+//   V  lane (g, t) reads the bytes of its 16 dims (16 g ..) of keys t, 4 + (t ^ 1), 8 + t, 12 + (t ^ 1);
+//      two keys' words are interleaved by a byte permute, then masked. pi (the order of the 16 keys
+//      along S^T's rows) makes these the keys 2t, 2t+1, 2t+8, 2t+9 of the P^T fragment; neighbours in
+//      it differ in parity, so the K reads are free of bank conflicts and the V reads two-way (64-byte
+//      rows).
 // P (times the key's V step) is rounded to f16 (11 bits; an fp32 sum keeps l and sum p lo) and turned
 // from accumulator to operand layout by movmatrix.
 // f16 range: Q is staged with its row maximum at 2^14 .. 2^15 and the factor kept in fp32. p is at most
@@ -32,8 +33,9 @@
 // Structure: 4 consumer warps and a producer warp per CTA, two CTAs per SM, taking items from the work
 // list. A block is one 64-key page: (codes, pairs) of K and of V are contiguous, one bulk copy each
 // (cp.async for ring rows, whose runs may start anywhere), several blocks ahead, across items. The
-// producer also hands over the item's geometry and its Q rows. Warps split a block's keys (and, for
-// more than 16 rows, the rows) and merge their softmax states at the end of the item.
+// producer also hands over the item's geometry and its Q rows. The warps take blocks in turn (for more
+// than 16 rows in pairs, half the rows each), 32 or 64 keys at a time so that enough independent MMAs are
+// in flight, and merge their softmax states at the end of the item.
 // Waits are bounded; a failing wait makes its warp return and the others run out theirs.
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -64,10 +66,39 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
+// mma_f16 with a zero accumulator.
+__device__ __forceinline__ void mma_f16_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 
-constexpr int I4_WARPS = 4;  // consumer warps
+#ifndef HSWA_I4_WARPS
+#define HSWA_I4_WARPS 4
+#endif
+#ifndef HSWA_I4_CTAS
+#define HSWA_I4_CTAS 2
+#endif
+#ifndef HSWA_I4_KU
+#define HSWA_I4_KU 2
+#endif
+#ifndef HSWA_I4_KU2
+#define HSWA_I4_KU2 2
+#endif
+#ifndef HSWA_I4_SUB
+#define HSWA_I4_SUB 1
+#endif
+#ifndef HSWA_I4_SUB2
+#define HSWA_I4_SUB2 1
+#endif
+constexpr int I4_WARPS = HSWA_I4_WARPS;  // consumer warps
+constexpr int I4_CTAS = HSWA_I4_CTAS;    // CTAs per SM
 constexpr int I4_THREADS = (I4_WARPS + 1) * 32;
 
 // One work item as the producer hands it to the consumers.
@@ -86,32 +117,38 @@ struct I4Smem {
   static constexpr int ROWS = 8 * NT * RG;
   static constexpr int BLK = (int)i4_block_bytes(64, D);
   static constexpr int STAGE = 2 * BLK;
-  static constexpr int NS = (RG == 2 ? 6 : 9) * (D == 128 ? 1 : 2);
   static constexpr int Q_BYTES = ROWS * D * 2;
   static constexpr int AREA_STRIDE = D + 4;  // floats
-  static constexpr int Q_OFF = NS * STAGE;
+  static constexpr int Q_OFF = 0;
   static constexpr int AREA_OFF = Q_OFF + 2 * Q_BYTES;
   static constexpr int ML_OFF = AREA_OFF + 2 * ROWS * AREA_STRIDE * 4;
-  // m, l, sum p lo per (warp, row); 2^E per warp; then m, 1/l or l, sum p lo per row
-  static constexpr int ITEM_OFF = ML_OFF + (3 * I4_WARPS * ROWS + I4_WARPS + 3 * ROWS) * 4;
+  // m, l, sum p lo per (warp, row), then per row
+  static constexpr int ITEM_OFF = ML_OFF + (3 * I4_WARPS * ROWS + 3 * ROWS) * 4;
+  static constexpr int MAX_NS = 32;
   static constexpr int BAR_OFF = (ITEM_OFF + 2 * (int)sizeof(I4Item) + 15) / 16 * 16;
-  static constexpr int BYTES = BAR_OFF + (2 * NS + 5) * 8 + 16;
-  static_assert(2 * (BYTES + 1024) <= 227 * 1024, "two CTAs per SM");
+  static constexpr int STAGE_OFF = (BAR_OFF + (2 * MAX_NS + 5) * 8 + 16 + 127) / 128 * 128;
+  // as many blocks in flight as the shared memory of I4_CTAS CTAs per SM allows
+  static constexpr int FIT = (227 * 1024 / I4_CTAS - 1024 - STAGE_OFF) / STAGE;
+  static constexpr int NS = FIT < MAX_NS ? FIT : MAX_NS;
+  static constexpr int BYTES = STAGE_OFF + NS * STAGE;
+  static_assert(NS >= 4, "blocks in flight");
 };
 
 template <int D, int NT, int RG, bool MOD>
-__global__ void __launch_bounds__(I4_THREADS, 2) decode_i4_kernel(DecParams p) {
+__global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParams p) {
   using SM = I4Smem<D, NT, RG>;
   constexpr int ROWS = SM::ROWS;
   constexpr int NS = SM::NS;
   constexpr int KW = I4_WARPS / RG;    // warps that share a row group
-  constexpr int KG = RG;               // 16-key groups per warp and block: 64 / 16 / KW
+  constexpr int SUB = NT == 1 ? HSWA_I4_SUB : HSWA_I4_SUB2;  // warps of a row group that share a block
+  constexpr int GW = 4 / SUB;          // 16-key groups of a block per warp
+  constexpr int KU = (NT == 1 ? HSWA_I4_KU : HSWA_I4_KU2) < GW ? (NT == 1 ? HSWA_I4_KU : HSWA_I4_KU2) : GW;  // in flight at once
   constexpr int NW = D / 32;           // 32-bit words of K codes per lane
   constexpr int MT = D / 16;           // m-tiles of O^T
   extern __shared__ __align__(128) uint8_t smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::BAR_OFF);
-  uint64_t* empty = full + NS;
-  uint64_t* item_full = empty + NS;
+  uint64_t* empty = full + SM::MAX_NS;
+  uint64_t* item_full = empty + SM::MAX_NS;
   uint64_t* item_empty = item_full + 2;
   uint64_t* cons = item_empty + 2;
   int* go = reinterpret_cast<int*>(cons + 1);
@@ -122,7 +159,7 @@ __global__ void __launch_bounds__(I4_THREADS, 2) decode_i4_kernel(DecParams p) {
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&full[i], 33);  // the producer's 32 lanes and its byte count
-      mbar_init(&empty[i], I4_WARPS);
+      mbar_init(&empty[i], RG * SUB);  // the warps that read a block
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&item_full[i], 1);
@@ -130,14 +167,28 @@ __global__ void __launch_bounds__(I4_THREADS, 2) decode_i4_kernel(DecParams p) {
     }
     mbar_init(cons, I4_WARPS);
     fence_barrier_init();
-    *go = read_error(p.err) == 0;
   }
+  grid_go();    // the merge may take its place; it waits for this grid's end before it reads
+  grid_wait();  // the work list
+  if (tid == 0) *go = read_error(p.err) == 0;
   __syncthreads();
   if (!*go) return;  // a pending device error: skip the work
 
   if (warp == I4_WARPS) {
     // ------------------------------------------------------------ producer
     const PlanView pv(p.ws, p.n_seqs);
+    int sp_L = 0, sp_body = 0, sp_excl = 0, total, body_total;
+    if (p.small) {
+      const SmallPlan sp(p);
+      sp_L = sp.L;
+      sp_body = sp.body;
+      sp_excl = sp.excl;
+      body_total = sp.total;
+      total = (sp.total + p.n_seqs) * p.Hkv;
+    } else {
+      body_total = hdr->body_total;
+      total = hdr->total_items;
+    }
     uint32_t cnt = 0;  // blocks issued
     int it = 0;
     bool ok = true;
@@ -145,10 +196,14 @@ __global__ void __launch_bounds__(I4_THREADS, 2) decode_i4_kernel(DecParams p) {
       const int slot = it & 1;
       if (!(ok = warp_wait(&item_empty[slot], ((it >> 1) & 1) ^ 1, p.err))) break;
       int item = 0;
-      if (lane == 0) item = atomicAdd(&hdr->counter, 1);
-      item = __shfl_sync(0xffffffffu, item, 0);
+      if (p.small) {
+        item = blockIdx.x + it * (int)gridDim.x;
+      } else {
+        if (lane == 0) item = atomicAdd(&hdr->counter, 1);
+        item = __shfl_sync(0xffffffffu, item, 0);
+      }
       I4Item& I = items[slot];
-      if (item >= hdr->total_items) {
+      if (item >= total || item < 0) {
         if (lane == 0) {
           I.item = -1;
           mbar_arrive(&item_full[slot]);
@@ -157,8 +212,20 @@ __global__ void __launch_bounds__(I4_THREADS, 2) decode_i4_kernel(DecParams p) {
       }
       const int g = item % p.Hkv;
       const int sc = item / p.Hkv;
-      int s, c;
-      if (sc < hdr->body_total) {
+      int s, c, L, nsp;
+      if (p.small) {
+        if (sc < body_total) {
+          // the last sequence whose prefix is not past sc (those without body splits share a prefix
+          // with their successor)
+          s = 31 - __clz(__ballot_sync(0xffffffffu, lane < p.n_seqs && sp_excl <= sc));
+          c = sc - __shfl_sync(0xffffffffu, sp_excl, s);
+        } else {
+          s = sc - body_total;
+          c = -1;
+        }
+        L = __shfl_sync(0xffffffffu, sp_L, s);
+        nsp = __shfl_sync(0xffffffffu, sp_body, s) + 1;
+      } else if (sc < body_total) {
         int lo = 0, hi = p.n_seqs;
         while (hi - lo > 1) {
           const int mid = (lo + hi) >> 1;
@@ -167,14 +234,16 @@ __global__ void __launch_bounds__(I4_THREADS, 2) decode_i4_kernel(DecParams p) {
         s = pv.order[lo];
         c = sc - pv.prefix[lo];
       } else {
-        s = pv.tail[sc - hdr->body_total];
+        s = pv.tail[sc - body_total];
         c = -1;
       }
-      const int L = (int)safe_len(p, s);
+      if (!p.small) {
+        L = (int)safe_len(p, s);
+        nsp = n_splits_x<true>(p, s, L);
+      }
       int64_t klo64, khi64;
       cached_range<true>(p, s, L, klo64, khi64);
       const int klo = (int)klo64, khi = (int)khi64;
-      const int nsp = n_splits_x<true>(p, s, L);
       if (c < 0) c = nsp - 1;
       const int a = klo + c * p.split;
       const int b = a + p.split < khi ? a + p.split : khi;
@@ -234,7 +303,7 @@ __global__ void __launch_bounds__(I4_THREADS, 2) decode_i4_kernel(DecParams p) {
           my_page = kb + lane < n_cached && lp < p.pt_stride ? pt_row[lp] : -1;
         }
         if (!(ok = warp_wait(&empty[st], ((cnt / NS) & 1) ^ 1, p.err))) break;
-        uint8_t* ks = smem + st * SM::STAGE;
+        uint8_t* ks = smem + SM::STAGE_OFF + st * SM::STAGE;
         uint8_t* vs = ks + SM::BLK;
         if (kb < n_cached && p.window <= 0) {
           const int page = __shfl_sync(0xffffffffu, my_page, kb & 31);
@@ -345,12 +414,12 @@ __global__ void __launch_bounds__(I4_THREADS, 2) decode_i4_kernel(DecParams p) {
   const int rg = RG == 2 ? warp & 1 : 0;
   const int kw = RG == 2 ? warp >> 1 : warp;
   const int row0 = rg * 8 * NT;
-  const int pi0 = (g8 >> 1) + 4 * (g8 & 1);  // key of S^T row g8 within a 16-key group (row g8 + 8: + 8)
+  // key of S^T row g8 within a 16-key group (row g8 + 8: + 8), see the header comment
+  const int pi0 = (g8 & 1) ? 4 + ((g8 >> 1) ^ 1) : g8 >> 1;
   float* m_w = reinterpret_cast<float*>(smem + SM::ML_OFF);  // [KW][ROWS]
   float* l_w = m_w + I4_WARPS * ROWS;
   float* b_w = l_w + I4_WARPS * ROWS;
-  float* e_w = b_w + I4_WARPS * ROWS;  // [I4_WARPS]
-  float* m_all = e_w + I4_WARPS;
+  float* m_all = b_w + I4_WARPS * ROWS;
   float* l_all = m_all + ROWS;
   float* b_all = l_all + ROWS;
   float* area = reinterpret_cast<float*>(smem + SM::AREA_OFF);  // [2][ROWS][AREA_STRIDE]
@@ -370,8 +439,7 @@ __global__ void __launch_bounds__(I4_THREADS, 2) decode_i4_kernel(DecParams p) {
 
     // ---- Q fragments: lane (g8, t4) holds dims [t4 D/4, +D/4) of row g8 of each n-tile
     uint32_t qf[NT][NW][4];
-    float c1[NT][2], c2[NT][2];
-    int r_lo[NT][2], r_hi[NT][2];
+    float c1[NT][2], c2[NT][2];  // score = c1 (acc * step + lo * c2)
     float slope[NT][2];
     int r_pos[NT][2];
 #pragma unroll
@@ -414,17 +482,14 @@ __global__ void __launch_bounds__(I4_THREADS, 2) decode_i4_kernel(DecParams p) {
         qf[nt][i][3] = pack_f16x2(hi(1), hi(3));
       }
       // scores from the accumulator: acc * 2^(e - 14 + 24) * step + lo * sum(q), times the softmax scale
-      const float sc = MOD ? p.scale_nat : p.scale_log2;
-      const float a1 = sc * pow2i(e + 10), a2 = sc * sum;
+      const float a1 = (MOD ? p.scale_nat : p.scale_log2) * pow2i(e + 10), a2 = sum * pow2i(-e - 10);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         c1[nt][c] = __shfl_sync(0xffffffffu, a1, (2 * t4 + c) * 4);
         c2[nt][c] = __shfl_sync(0xffffffffu, a2, (2 * t4 + c) * 4);
-        const int rr = row0 + nt * 8 + 2 * t4 + c;
-        const int tok = rr < p.R ? rr / p.G : 0;
-        r_lo[nt][c] = I.row_lo[tok];
-        r_hi[nt][c] = I.row_hi[tok];
         if constexpr (MOD) {
+          const int rr = row0 + nt * 8 + 2 * t4 + c;
+          const int tok = rr < p.R ? rr / p.G : 0;
           r_pos[nt][c] = L + tok;
           slope[nt][c] = p.slope && rr < p.R ? p.slope[I.g * p.G + rr % p.G] * 1.4426950408889634f : 0.f;
         }
@@ -446,25 +511,30 @@ __global__ void __launch_bounds__(I4_THREADS, 2) decode_i4_kernel(DecParams p) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
     int e_cur = -120;        // V steps are used divided by 2^e_cur
+    float fe = pow2i(120);   // 2^-e_cur
     float sv_lim = -1.f;     // a step above this moves e_cur
+    const int lo_min = I.lo_min, lo_max = I.lo_max, hi_min = I.hi_min;
 
-    for (int kb = 0; kb < n_blk; ++kb, ++cnt) {
-      const int st = cnt % NS;
-      if (!warp_wait(&full[st], (cnt / NS) & 1, p.err)) return;
-      uint8_t* ks = smem + st * SM::STAGE;
+    for (int kb = kw / SUB; kb < n_blk; kb += KW / SUB) {
+      const uint32_t cb = cnt + kb;
+      const int st = cb % NS;
+      if (!warp_wait(&full[st], (cb / NS) & 1, p.err)) return;
+      uint8_t* ks = smem + SM::STAGE_OFF + st * SM::STAGE;
       uint8_t* vs = ks + SM::BLK;
       const bool is_new = kb >= n_cached;
       const int kbase = is_new ? L : ia + kb * 64;
       const int kend = is_new ? L + p.n_qt : ib;  // no key at or past this
-      const bool edge = kbase + 64 > min(kend, I.hi_min) || kbase < I.lo_max;
+      const bool edge = kbase + 64 > min(kend, hi_min) || kbase < lo_max;
+#pragma unroll 1
+      for (int k0 = (kw % SUB) * 16 * GW; k0 < (kw % SUB + 1) * 16 * GW; k0 += 16 * KU) {
+        if (edge && (kbase + k0 >= kend || kbase + k0 + 16 * KU <= lo_min)) continue;  // nothing here
+        // ---- S^T = K Q^T, KU groups of 16 keys
+        float acc[KU][NT][4];
+        uint32_t kp[KU][2], vp[KU][2];
 #pragma unroll
-      for (int kg = 0; kg < KG; ++kg) {
-        const int key0 = (kw * KG + kg) * 16;
-        const int kpos = kbase + key0;
-        if (edge && (kpos >= kend || kpos + 16 <= I.lo_min)) continue;  // nothing in this group
-        // ---- S^T = K Q^T
-        uint32_t wl[NW], wh[NW];
-        {
+        for (int u = 0; u < KU; ++u) {
+          const int key0 = k0 + 16 * u;
+          uint32_t wl[NW], wh[NW];
           const uint8_t* a0 = i4_codes<D>(ks, key0 + pi0) + t4 * (D / 8);
           if constexpr (D == 128) {
             const uint4 x = *reinterpret_cast<const uint4*>(a0), y = *reinterpret_cast<const uint4*>(a0 + 8 * (D / 2));
@@ -475,55 +545,89 @@ __global__ void __launch_bounds__(I4_THREADS, 2) decode_i4_kernel(DecParams p) {
             wl[0] = x.x; wl[1] = x.y;
             wh[0] = y.x; wh[1] = y.y;
           }
+          kp[u][0] = *i4_pair<D>(ks, 64, key0 + pi0);
+          kp[u][1] = *i4_pair<D>(ks, 64, key0 + pi0 + 8);
+          vp[u][0] = *i4_pair<D>(vs, 64, key0 + pi0);
+          vp[u][1] = *i4_pair<D>(vs, 64, key0 + pi0 + 8);
+#pragma unroll
+          for (int i = 0; i < NW; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t x = wl[i] >> (8 * h), y = wh[i] >> (8 * h);
+              const uint32_t a0 = x & 0x000F000Fu, a1 = y & 0x000F000Fu, a2 = x & 0x00F000F0u, a3 = y & 0x00F000F0u;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                if (i == 0 && h == 0)
+                  mma_f16_zero(acc[u][nt], a0, a1, a2, a3, qf[nt][0][0], qf[nt][0][1]);
+                else
+                  mma_f16(acc[u][nt], a0, a1, a2, a3, qf[nt][i][2 * h], qf[nt][i][2 * h + 1]);
+              }
+            }
         }
-        uint32_t kp[2] = {*i4_pair<D>(ks, 64, key0 + pi0), *i4_pair<D>(ks, 64, key0 + pi0 + 8)};
-        uint32_t vp[2] = {*i4_pair<D>(vs, 64, key0 + pi0), *i4_pair<D>(vs, 64, key0 + pi0 + 8)};
         if (edge) {  // rows no query row sees may hold anything: they stand for zero
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int key = kpos + pi0 + 8 * k;
-            if (key >= kend || key < I.lo_min) kp[k] = vp[k] = 0u;
-          }
+          for (int u = 0; u < KU; ++u)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int key = kbase + k0 + 16 * u + pi0 + 8 * k;
+              if (key >= kend || key < lo_min) kp[u][k] = vp[u][k] = 0u;
+            }
         }
-        float acc[NT][4];
+        // ---- scores in the log2 domain, masks
+        bool move = false;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+        for (int u = 0; u < KU; ++u) {
 #pragma unroll
-        for (int i = 0; i < NW; ++i)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t x = wl[i] >> (8 * h), y = wh[i] >> (8 * h);
-            const uint32_t a0 = x & 0x000F000Fu, a1 = y & 0x000F000Fu, a2 = x & 0x00F000F0u, a3 = y & 0x00F000F0u;
+          for (int k = 0; k < 2; ++k) {
+            const float ksf = __uint_as_float(kp[u][k] << 16), klf = __uint_as_float(kp[u][k] & 0xFFFF0000u);
+            move = move || __uint_as_float(vp[u][k] << 16) > sv_lim;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma_f16(acc[nt], a0, a1, a2, a3, qf[nt][i][2 * h], qf[nt][i][2 * h + 1]);
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                float z = fmaf(acc[u][nt][2 * k + c], ksf, klf * c2[nt][c]);
+                if constexpr (MOD) {
+                  const int key = kbase + k0 + 16 * u + pi0 + 8 * k;
+                  z *= c1[nt][c];
+                  z = p.softcap > 0.f ? capped_log2(z, p.cap_in, p.cap_log2) : z * 1.4426950408889634f;
+                  if (p.slope) z = fmaf(-slope[nt][c], (float)abs(r_pos[nt][c] - key), z);
+                }
+                acc[u][nt][2 * k + c] = z;
+              }
           }
-        // ---- scores in the log2 domain, masks, softmax weights
-        const float ksf[2] = {__uint_as_float(kp[0] << 16), __uint_as_float(kp[1] << 16)};
-        const float klf[2] = {__uint_as_float(kp[0] & 0xFFFF0000u), __uint_as_float(kp[1] & 0xFFFF0000u)};
-        float vsf[2] = {__uint_as_float(vp[0] << 16), __uint_as_float(vp[1] << 16)};
-        const float vlf[2] = {__uint_as_float(vp[0] & 0xFFFF0000u), __uint_as_float(vp[1] & 0xFFFF0000u)};
-        bool move = vsf[0] > sv_lim || vsf[1] > sv_lim;
+        }
+        if (edge) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int rr = row0 + nt * 8 + 2 * t4 + c;
+              const int tok = rr < p.R ? rr / p.G : 0;
+              const int r_lo = I.row_lo[tok], r_hi = min(I.row_hi[tok], kend);
+#pragma unroll
+              for (int u = 0; u < KU; ++u)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const int key = kbase + k0 + 16 * u + pi0 + 8 * k;
+                  if (key < r_lo || key >= r_hi) acc[u][nt][2 * k + c] = -INFINITY;
+                }
+            }
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int k = x >> 1, c = x & 1;
-            float z = fmaf(acc[nt][x] * ksf[k], c1[nt][c], klf[k] * c2[nt][c]);
-            if constexpr (MOD) {
-              const int key = kpos + pi0 + 8 * k;
-              z = p.softcap > 0.f ? capped_log2(z, p.cap_in, p.cap_log2) : z * 1.4426950408889634f;
-              if (p.slope) z = fmaf(-slope[nt][c], (float)abs(r_pos[nt][c] - key), z);
-            }
-            if (edge) {
-              const int key = kpos + pi0 + 8 * k;
-              if (key < r_lo[nt][c] || key >= r_hi[nt][c] || key >= kend) z = -INFINITY;
-            }
-            acc[nt][x] = z;
-            move = move || z > m[nt][c] + 8.f;
+          for (int c = 0; c < 2; ++c) {
+            float mx = fmaxf(acc[0][nt][c], acc[0][nt][2 + c]);
+#pragma unroll
+            for (int u = 1; u < KU; ++u) mx = fmax3(mx, acc[u][nt][c], acc[u][nt][2 + c]);
+            if constexpr (!MOD) mx *= c1[nt][c];
+            move = move || mx > m[nt][c] + 8.f;
           }
         if (__any_sync(0xffffffffu, move)) {
-          float smax = fmaxf(vsf[0], vsf[1]);
+          float smax = 0.f;
+#pragma unroll
+          for (int u = 0; u < KU; ++u)
+            smax = fmax3(smax, __uint_as_float(vp[u][0] << 16), __uint_as_float(vp[u][1] << 16));
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, x));
           float osc = 1.f;
@@ -533,6 +637,7 @@ __global__ void __launch_bounds__(I4_THREADS, 2) decode_i4_kernel(DecParams p) {
             if (e > e_cur) {
               osc = e - e_cur > 126 ? 0.f : pow2i(e_cur - e);
               e_cur = e;
+              fe = pow2i(-e_cur);
             }
             sv_lim = e_cur >= 120 ? 3.4e38f : pow2i(e_cur + 7);
           }
@@ -540,9 +645,12 @@ __global__ void __launch_bounds__(I4_THREADS, 2) decode_i4_kernel(DecParams p) {
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              float mx = fmaxf(acc[nt][c], acc[nt][2 + c]);
+              float mx = fmaxf(acc[0][nt][c], acc[0][nt][2 + c]);
+#pragma unroll
+              for (int u = 1; u < KU; ++u) mx = fmax3(mx, acc[u][nt][c], acc[u][nt][2 + c]);
 #pragma unroll
               for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+              if constexpr (!MOD) mx *= c1[nt][c];
               const float mn = fmaxf(m[nt][c], mx);
               const float al = mn == -INFINITY ? 1.f : ex2_approx(m[nt][c] - mn);
               m[nt][c] = mn;
@@ -556,33 +664,40 @@ __global__ void __launch_bounds__(I4_THREADS, 2) decode_i4_kernel(DecParams p) {
               }
             }
         }
-        const float fe = pow2i(-e_cur);
-        vsf[0] *= fe;
-        vsf[1] *= fe;
-        uint32_t pb[NT][2];
+        // ---- softmax weights, O^T += V^T P^T
+        float moff[NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float w[4];
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int k = x >> 1, c = x & 1;
-            const float moff = m[nt][c] == -INFINITY ? 0.f : m[nt][c];
-            const float e = ex2_approx(acc[nt][x] - moff);
-            l[nt][c] += e;
-            bs[nt][c] = fmaf(e, vlf[k], bs[nt][c]);
-            w[x] = e * vsf[k];
+          for (int c = 0; c < 2; ++c) moff[nt][c] = m[nt][c] == -INFINITY ? 0.f : m[nt][c];
+#pragma unroll
+        for (int u = 0; u < KU; ++u) {
+          uint32_t pb[NT][2];
+          const float vsf[2] = {__uint_as_float(vp[u][0] << 16) * fe, __uint_as_float(vp[u][1] << 16) * fe};
+          const float vlf[2] = {__uint_as_float(vp[u][0] & 0xFFFF0000u), __uint_as_float(vp[u][1] & 0xFFFF0000u)};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float w[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int k = x >> 1, c = x & 1;
+              const float e =
+                  ex2_approx(MOD ? acc[u][nt][x] - moff[nt][c] : fmaf(acc[u][nt][x], c1[nt][c], -moff[nt][c]));
+              l[nt][c] += e;
+              bs[nt][c] = fmaf(e, vlf[k], bs[nt][c]);
+              w[x] = e * vsf[k];
+            }
+            pb[nt][0] = movmatrix_t(pack_f16x2(w[0], w[1]));
+            pb[nt][1] = movmatrix_t(pack_f16x2(w[2], w[3]));
           }
-          pb[nt][0] = movmatrix_t(pack_f16x2(w[0], w[1]));
-          pb[nt][1] = movmatrix_t(pack_f16x2(w[2], w[3]));
-        }
-        // ---- O^T += V^T P^T: this lane's dims [g8 D/8, +D/8) of keys t4, 4 + t4, 8 + t4, 12 + t4
-        {
-          const uint8_t* v0 = i4_codes<D>(vs, key0 + t4) + g8 * (D / 16);
+          // this lane's dims [g8 D/8, +D/8) of keys t4, 4 + (t4 ^ 1) and the same + 8
+          const uint8_t* v0 = i4_codes<D>(vs, k0 + 16 * u + t4) + g8 * (D / 16);
+          const uint8_t* v1 = i4_codes<D>(vs, k0 + 16 * u + 4 + (t4 ^ 1)) + g8 * (D / 16);
           constexpr int VW = D / 64;  // words per key
           uint32_t vw[4][VW];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint8_t* src = v0 + 4 * j * (D / 2);
+            const uint8_t* src = ((j & 1) ? v1 : v0) + (j >> 1) * 8 * (D / 2);
             if constexpr (VW == 2) {
               const uint2 x = *reinterpret_cast<const uint2*>(src);
               vw[j][0] = x.x;
@@ -595,7 +710,7 @@ __global__ void __launch_bounds__(I4_THREADS, 2) decode_i4_kernel(DecParams p) {
           for (int h = 0; h < VW; ++h)
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              // four dims (8h + 4q ..) of the key pairs (t4, 4 + t4) and (8 + t4, 12 + t4)
+              // four dims (8h + 4q ..) of the two key pairs
               const uint32_t u0 = __byte_perm(vw[0][h], vw[1][h], q ? 0x7632u : 0x5410u);
               const uint32_t u1 = __byte_perm(vw[2][h], vw[3][h], q ? 0x7632u : 0x5410u);
 #pragma unroll
@@ -613,6 +728,7 @@ __global__ void __launch_bounds__(I4_THREADS, 2) decode_i4_kernel(DecParams p) {
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
     }
+    cnt += n_blk;
 
     // ---- merge the warps' states
     const int s = I.s, hg = I.g, nsp = I.nsp, item = I.item;
@@ -689,10 +805,9 @@ __global__ void __launch_bounds__(I4_THREADS, 2) decode_i4_kernel(DecParams p) {
             }
           }
       };
-      if (kw < 2) put(false);
-      if (!cons_sync()) return;
-      if constexpr (KW == 4) {
-        if (kw >= 2) put(true);
+#pragma unroll 1
+      for (int rnd = 0; rnd < KW / 2; ++rnd) {  // two warps of a row group at a time, one per area
+        if ((kw >> 1) == rnd) put(rnd > 0);
         if (!cons_sync()) return;
       }
     }

@@ -97,6 +97,20 @@ int check_device(const hswa_pool* pool, const char* who) {
   return HSWA_OK;
 }
 
+int current_sms(const char* who, int* sms) {
+  static std::atomic<int> known[64];
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && dev < 64 && (*sms = known[dev].load(std::memory_order_relaxed)) > 0) return HSWA_OK;
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) {
+    set_error("%s: no current CUDA device: %s", who, cudaGetErrorString(e));
+    return HSWA_ERR_CUDA;
+  }
+  if (dev < 64) known[dev].store(*sms, std::memory_order_relaxed);
+  return HSWA_OK;
+}
+
 static int check_desc(const hswa_pool_desc* d) {
   if (!d) {
     set_error("null pool descriptor");
@@ -394,17 +408,6 @@ static int check_rope(const hswa_rope_desc* r, int head_dim, const char* who) {
       set_error("%s: pair %d has axis %d of %d or a frequency that is not finite", who, i, (int)r->axis[i], r->n_axes);
       return HSWA_ERR_INVALID_ARG;
     }
-  return HSWA_OK;
-}
-
-static int current_sms(const char* who, int* sms) {
-  int dev = -1;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) {
-    set_error("%s: no current CUDA device: %s", who, cudaGetErrorString(e));
-    return HSWA_ERR_CUDA;
-  }
   return HSWA_OK;
 }
 
@@ -747,8 +750,12 @@ int prepare_decode(hswa_pool* pool, const char* who, int layer, const uint16_t* 
   }
   const int window = is_swa ? D.window : 0;
   const bool ext = pool->i4 || mod;
-  const size_t msm = decode_merge_smem_bytes(n_seqs, n_q_per_seq, n_q_heads, D.n_kv_heads, window, max_ctx_len, ext);
-  if (msm > (size_t)pool->smem_optin) {
+  if (ext && decode_max_items(n_seqs, D.n_kv_heads, window, max_ctx_len, ext) > 0x7fffffffLL) {
+    set_error("%s: too many splits for 32-bit work items", who);
+    return HSWA_ERR_UNSUPPORTED_SHAPE;
+  }
+  const size_t msm = decode_merge_smem_bytes(n_seqs, n_q_per_seq, n_q_heads, D.n_kv_heads, window, max_ctx_len);
+  if (!ext && msm > (size_t)pool->smem_optin) {
     set_error("%s: max_ctx_len %lld gives %zu bytes of split-merge shared memory; this device allows %d", who,
               (long long)max_ctx_len, msm, pool->smem_optin);
     return HSWA_ERR_UNSUPPORTED_SHAPE;

@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/hswa.h"
 
 struct hswa_pool {
@@ -47,6 +49,21 @@ void set_error(const char* fmt, ...);
 // HSWA_OK when the calling thread's current CUDA device is the pool's device; otherwise
 // HSWA_ERR_INVALID_ARG with a message naming `who` (nothing may be launched for the call).
 int check_device(const hswa_pool* pool, const char* who);
+
+// The multiprocessor count of the current device (looked up once per device); HSWA_ERR_CUDA on failure.
+int current_sms(const char* who, int* sms);
+
+// cudaFuncSetAttribute(MaxDynamicSharedMemorySize) once per kernel and device: `done` is the kernel's own
+// static bit mask over devices (devices past 63 set it every time).
+#define HSWA_SET_SMEM(kernel, bytes, device)                                                          \
+  do {                                                                                                \
+    static std::atomic<unsigned long long> done{0};                                                   \
+    const unsigned long long bit = (device) < 64 ? 1ull << (device) : 0ull;                           \
+    if (!(done.load(std::memory_order_relaxed) & bit) || !bit) {                                      \
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(bytes));        \
+      done.fetch_or(bit, std::memory_order_relaxed);                                                  \
+    }                                                                                                 \
+  } while (0)
 
 // Encode a 2-5 dimensional bf16 tiled tensor map with 128-byte swizzle.
 // dims/strides: innermost first; strides in bytes for dims 1.. (dim 0 is contiguous).
@@ -149,7 +166,9 @@ struct DecodeLaunch {
 
 size_t decode_workspace_bytes(int n_seqs, int n_qt, int Hq, int Hkv, int d, int window, int64_t max_ctx_len, bool ext);
 // Dynamic shared memory of the split merge for these arguments (0 when no sequence can have two splits).
-size_t decode_merge_smem_bytes(int n_seqs, int n_qt, int Hq, int Hkv, int window, int64_t max_ctx_len, bool ext);
+size_t decode_merge_smem_bytes(int n_seqs, int n_qt, int Hq, int Hkv, int window, int64_t max_ctx_len);
+// Work items a call may have at most (a split of one KV head of one sequence each).
+int64_t decode_max_items(int n_seqs, int Hkv, int window, int64_t max_ctx_len, bool ext);
 
 // Argument checks shared by hybrid_decode_fwd and hybrid_decode_fwd_noalloc (messages name `who`).
 // On HSWA_OK, *L is filled except for workspace/ws_bytes and *need is the scratch the call uses;
