@@ -79,27 +79,22 @@ __device__ __forceinline__ void mma_f16_zero(float (&c)[4], uint32_t a0, uint32_
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 
-#ifndef HSWA_I4_WARPS
-#define HSWA_I4_WARPS 4
+#ifndef HSWA_I4_CFG1
+#define HSWA_I4_CFG1 0x4221
 #endif
-#ifndef HSWA_I4_CTAS
-#define HSWA_I4_CTAS 2
+#ifndef HSWA_I4_CFG2
+#define HSWA_I4_CFG2 0x4221
 #endif
-#ifndef HSWA_I4_KU
-#define HSWA_I4_KU 2
-#endif
-#ifndef HSWA_I4_KU2
-#define HSWA_I4_KU2 2
-#endif
-#ifndef HSWA_I4_SUB
-#define HSWA_I4_SUB 1
-#endif
-#ifndef HSWA_I4_SUB2
-#define HSWA_I4_SUB2 1
-#endif
-constexpr int I4_WARPS = HSWA_I4_WARPS;  // consumer warps
-constexpr int I4_CTAS = HSWA_I4_CTAS;    // CTAs per SM
-constexpr int I4_THREADS = (I4_WARPS + 1) * 32;
+template <int X>
+struct I4CfgT {
+  static constexpr int W = X >> 12;            // consumer warps per CTA
+  static constexpr int CTAS = (X >> 8) & 15;   // CTAs per SM
+  static constexpr int KU = (X >> 4) & 15;     // 16-key groups in flight at once in a warp
+  static constexpr int SUB = X & 15;           // warps of a row group that share a block
+  static constexpr int THREADS = (W + 1) * 32;
+};
+template <int NT> struct I4Cfg : I4CfgT<HSWA_I4_CFG1> {};
+template <> struct I4Cfg<2> : I4CfgT<HSWA_I4_CFG2> {};
 
 // One work item as the producer hands it to the consumers.
 struct I4Item {
@@ -114,6 +109,7 @@ struct I4Item {
 
 template <int D, int NT, int RG>
 struct I4Smem {
+  using CFG = I4Cfg<NT>;
   static constexpr int ROWS = 8 * NT * RG;
   static constexpr int BLK = (int)i4_block_bytes(64, D);
   static constexpr int STAGE = 2 * BLK;
@@ -123,26 +119,30 @@ struct I4Smem {
   static constexpr int AREA_OFF = Q_OFF + 2 * Q_BYTES;
   static constexpr int ML_OFF = AREA_OFF + 2 * ROWS * AREA_STRIDE * 4;
   // m, l, sum p lo per (warp, row), then per row
-  static constexpr int ITEM_OFF = ML_OFF + (3 * I4_WARPS * ROWS + 3 * ROWS) * 4;
+  static constexpr int ROW_OFF = ML_OFF + (3 * CFG::W * ROWS + 3 * ROWS) * 4;  // per row: token, output offset
+  static constexpr int ITEM_OFF = ROW_OFF + 2 * ROWS * 4;
   static constexpr int MAX_NS = 32;
   static constexpr int BAR_OFF = (ITEM_OFF + 2 * (int)sizeof(I4Item) + 15) / 16 * 16;
   static constexpr int STAGE_OFF = (BAR_OFF + (2 * MAX_NS + 5) * 8 + 16 + 127) / 128 * 128;
-  // as many blocks in flight as the shared memory of I4_CTAS CTAs per SM allows
-  static constexpr int FIT = (227 * 1024 / I4_CTAS - 1024 - STAGE_OFF) / STAGE;
+  // as many blocks in flight as the shared memory of CTAS CTAs per SM allows
+  static constexpr int FIT = (227 * 1024 / CFG::CTAS - 1024 - STAGE_OFF) / STAGE;
   static constexpr int NS = FIT < MAX_NS ? FIT : MAX_NS;
   static constexpr int BYTES = STAGE_OFF + NS * STAGE;
   static_assert(NS >= 4, "blocks in flight");
 };
 
 template <int D, int NT, int RG, bool MOD>
-__global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParams p) {
+__global__ void __launch_bounds__(I4Cfg<NT>::THREADS, I4Cfg<NT>::CTAS) decode_i4_kernel(DecParams p) {
   using SM = I4Smem<D, NT, RG>;
   constexpr int ROWS = SM::ROWS;
   constexpr int NS = SM::NS;
+  using CFG = I4Cfg<NT>;
+  constexpr int I4_WARPS = CFG::W;
   constexpr int KW = I4_WARPS / RG;    // warps that share a row group
-  constexpr int SUB = NT == 1 ? HSWA_I4_SUB : HSWA_I4_SUB2;  // warps of a row group that share a block
+  constexpr int SUB = CFG::SUB;
   constexpr int GW = 4 / SUB;          // 16-key groups of a block per warp
-  constexpr int KU = (NT == 1 ? HSWA_I4_KU : HSWA_I4_KU2) < GW ? (NT == 1 ? HSWA_I4_KU : HSWA_I4_KU2) : GW;  // in flight at once
+  constexpr int KU = CFG::KU < GW ? CFG::KU : GW;
+  static_assert(KW % SUB == 0, "warps share blocks evenly");
   constexpr int NW = D / 32;           // 32-bit words of K codes per lane
   constexpr int MT = D / 16;           // m-tiles of O^T
   extern __shared__ __align__(128) uint8_t smem[];
@@ -156,6 +156,13 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   WsHeader* hdr = reinterpret_cast<WsHeader*>(p.ws);
 
+  int* row_tok = reinterpret_cast<int*>(smem + SM::ROW_OFF);  // new token of a query row
+  int* row_out = row_tok + ROWS;  // its place in the output, from (sequence, first token, first head of g)
+  for (int r = tid; r < ROWS; r += CFG::THREADS) {
+    const int t = r < p.R ? r / p.G : 0;
+    row_tok[r] = t;
+    row_out[r] = (t * p.Hq + (r - t * p.G)) * D;
+  }
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&full[i], 33);  // the producer's 32 lanes and its byte count
@@ -489,7 +496,7 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
         c2[nt][c] = __shfl_sync(0xffffffffu, a2, (2 * t4 + c) * 4);
         if constexpr (MOD) {
           const int rr = row0 + nt * 8 + 2 * t4 + c;
-          const int tok = rr < p.R ? rr / p.G : 0;
+          const int tok = row_tok[rr];
           r_pos[nt][c] = L + tok;
           slope[nt][c] = p.slope && rr < p.R ? p.slope[I.g * p.G + rr % p.G] * 1.4426950408889634f : 0.f;
         }
@@ -601,8 +608,7 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const int rr = row0 + nt * 8 + 2 * t4 + c;
-              const int tok = rr < p.R ? rr / p.G : 0;
+              const int tok = row_tok[row0 + nt * 8 + 2 * t4 + c];
               const int r_lo = I.row_lo[tok], r_hi = min(I.row_hi[tok], kend);
 #pragma unroll
               for (int u = 0; u < KU; ++u)
@@ -806,7 +812,7 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
           }
       };
 #pragma unroll 1
-      for (int rnd = 0; rnd < KW / 2; ++rnd) {  // two warps of a row group at a time, one per area
+      for (int rnd = 0; rnd < (KW + 1) / 2; ++rnd) {  // two warps of a row group at a time, one per area
         if ((kw >> 1) == rnd) put(rnd > 0);
         if (!cons_sync()) return;
       }
@@ -819,6 +825,8 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
       return make_float4(x.x + y.x + bb, x.y + y.y + bb, x.z + y.z + bb, x.w + y.w + bb);
     };
     float* part = reinterpret_cast<float*>(p.ws + p.part_off + (size_t)item * p.part_bytes);
+    uint16_t* out = p.o + ((int64_t)s * p.n_qt * p.Hq + hg * p.G) * D;
+#pragma unroll 4
     for (int idx = tid; idx < p.R * (D / 4); idx += I4_WARPS * 32) {
       const int r = idx / (D / 4), c = (idx % (D / 4)) * 4;
       float4 x = merged4(r, c);
@@ -827,11 +835,10 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
         const float inv = 1.f / ls;
         if (ls == 0.f) x = make_float4(0.f, 0.f, 0.f, 0.f);  // a row that sees nothing
         else x = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
-        const int t = r / p.G, hh = r % p.G;
         uint2 pk;
         pk.x = pack_bf16x2(x.x, x.y);
         pk.y = pack_bf16x2(x.z, x.w);
-        *reinterpret_cast<uint2*>(p.o + (((int64_t)s * p.n_qt + t) * p.Hq + hg * p.G + hh) * D + c) = pk;
+        *reinterpret_cast<uint2*>(out + row_out[r] + c) = pk;
       } else {
         *reinterpret_cast<float4*>(part + r * D + c) = x;
       }

@@ -51,8 +51,19 @@ namespace {
 
 constexpr int NQT = 2;      // query tiles per unit
 constexpr int NSTAGE = 2;   // K/V pipeline depth
+constexpr int NRAWK = 2;    // raw 4-bit K tiles ahead of it,
+constexpr int NRAW = NRAWK + 1;  // and one V tile
 constexpr int NWARPS = 12;         // 3 warpgroups: registers are granted per warpgroup
 constexpr int NTHREADS = NWARPS * 32;
+// 4-bit pools: a fourth warpgroup converts the page tiles, one warp per scheduler
+constexpr int NTHREADS_I4 = NTHREADS + 128;
+#ifndef HSWA_SOFTMAX_REGS_I4
+#define HSWA_SOFTMAX_REGS_I4 200
+#endif
+#ifndef HSWA_PRODUCER_REGS_I4
+#define HSWA_PRODUCER_REGS_I4 56
+#endif
+static_assert(2 * 128 * HSWA_SOFTMAX_REGS_I4 + 256 * HSWA_PRODUCER_REGS_I4 <= 512 * 128, "register split");
 constexpr int PRODUCER_WARP = 8;
 constexpr int MMA_WARP = 9;
 
@@ -64,6 +75,7 @@ struct Params {
   const int32_t* seq_ids;
   const int32_t* page_table;
   int pt_stride;
+  uint16_t* o;
   const uint16_t* ring_k;
   const uint16_t* ring_v;
   const uint8_t* ring_k8;  // FP8 pools: the rings as E4M3 codes, and this layer's per-KV-head scales
@@ -218,19 +230,22 @@ struct Layout {
   static constexpr int V_OFF = K_OFF + NSTAGE * TILE;
   static constexpr int O_OFF = V_OFF + NSTAGE * TILE;   // output staging: 4 KB (32 rows x 128 B) per softmax warp
   static constexpr int BAR_OFF = O_OFF + 2 * BLOCK;
-  static constexpr int BYTES = BAR_OFF + 256;
+  static constexpr int BYTES = BAR_OFF + 384;
   static_assert(BYTES + 1024 <= 227 * 1024, "shared memory per CTA");
+  static_assert(NRAW * 2 * i4_block_bytes(64, D) <= 2 * BLOCK, "raw 4-bit tiles lie in the output staging");
   static constexpr int O_COL0 = 256;
   static constexpr int O_STRIDE = 128;
 };
 
-struct Bars {
+struct Bars {  // at most 384 bytes
   uint64_t q_full, q_empty;
+  uint64_t q_ready;  // 4-bit pages: Q's dims are in the converted tiles' order
   uint64_t k_full[NSTAGE], k_empty[NSTAGE], v_full[NSTAGE], v_empty[NSTAGE];
   uint64_t raw_k[NSTAGE], raw_v[NSTAGE];  // FP8 page tiles landed (before conversion)
   uint64_t s_full[NQT], p_full[NQT], o_full[NQT];
+  uint64_t raw_full[NRAW], raw_empty[NRAW];  // 4-bit page tiles: copied, converted
+  uint32_t half_ok[NRAW];                    // which 64-row halves of the raw tile were copied
   uint64_t v_fix;  // TMA completion of the page tile that holds the last key (before its tail is zeroed)
-  uint32_t half_ok[2][NSTAGE];  // 4-bit pages: which 64-row halves of a raw tile (K, V) were copied
   uint32_t tmem_base;
 };
 
@@ -483,65 +498,112 @@ __device__ void page_converter(const Params& p, uint8_t* smem, Bars* bars) {
   }
 }
 
-// 4-bit page tiles (full layers of a 4-bit pool): the producer copies the two page blocks of a tile (64
-// rows of codes and their pairs, contiguous in HBM, one bulk copy each) into the stage buffer; warp
-// 10 + h turns half h into bf16. The raw block lies in the 8 KB of the buffer that the half's own upper
-// (head_dim 64: only) block rows take afterwards, so a warp reads its rows' codes and pairs into registers
-// (two rows per lane), meets at the warp barrier, and then writes; the two halves do not touch. Six
-// instructions per pair of values, about 1500 per lane and pair of K and V tiles, in the shadow of the
-// tile's MMAs and softmax. Rows no query of the unit sees, and those of a bad page, become zeros.
+// 4-bit page tiles (full layers of a 4-bit pool). The producer copies the two page blocks of a tile (64
+// rows of codes and their pairs, contiguous in HBM, one bulk copy each) into raw buffers, two for K tiles
+// and one for V tiles, which lie where the output is staged otherwise (these units store O from
+// registers). A fourth warpgroup turns them into bf16 rows of the stage buffers: two warps make the K
+// tiles and two the V tiles, half a tile each, so that a K tile does not wait behind a V tile whose stage
+// is still being read. Measured on a 2048-row chunk after 30000 keys (bf16 pages 983 us): two warps making
+// K and V in turn from raw copies inside the stage buffers 1700 us; four, unrolled, 1709; this loop 1187.
+// Integer instructions are what a conversion costs (two clocks each per scheduler), so the eight dims of a
+// word stay in the order in which one shift and one mask take them (0 4 1 5 2 6 3 7): the same warps put
+// Q's dims in that order once per unit, and the epilogue puts O's columns back. Rows no query of the unit sees, and those of
+// a bad page, become zeros.
 template <int D, bool MOD>
-__device__ void page_converter_i4(const Params& p, uint8_t* smem, Bars* bars) {
+__device__ void page_converter_i4(const Params& p, uint8_t* smem, Bars* bars, const int kv, const int half) {
   using L = Layout<D>;
   constexpr int NC = D / 32;  // 16-byte chunks of codes per row
   const int lane = threadIdx.x & 31;
-  const int half = (threadIdx.x >> 5) - 10;
-  int it = 0;
-  for (int rnd = 0, unit = cta_unit(0); unit < p.n_units; unit = cta_unit(++rnd)) {
+  uint32_t it = 0, uq = 0;
+  for (int rnd = 0, unit = cta_unit(0); unit < p.n_units; unit = cta_unit(++rnd), ++uq) {
     Geo G;
     make_geo<MOD>(p, unit, G);
+    // Q's dims in the order of the converted tiles (any order common to Q and K gives the same products)
+    if (!__all_sync(0xffffffffu, mbar_wait(&bars->q_full, uq & 1, p.err))) return;
+    for (int i = threadIdx.x & 127; i < NQT * L::TILE / 16; i += 128) {
+      uint4* q = reinterpret_cast<uint4*>(smem + L::Q_OFF) + i;
+      const uint4 x = *q;
+      *q = make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632), __byte_perm(x.y, x.w, 0x5410),
+                      __byte_perm(x.y, x.w, 0x7632));
+    }
+    fence_proxy_async_smem();
+    mbar_arrive(&bars->q_ready);
     for (int j = G.jb; j <= G.je; ++j, ++it) {
       const int s = it % NSTAGE;
-      const uint32_t ph = (it / NSTAGE) & 1;
+      const int rs = kv ? NRAWK : it % NRAWK;
+      const uint32_t rph = kv ? it : it / NRAWK;
       const int kb = key_base(p, G, j) + 64 * half;
-      for (int kv = 0; kv < 2; ++kv) {
-        if (!mbar_wait(kv ? &bars->raw_v[s] : &bars->raw_k[s], ph, p.err)) return;
-        uint8_t* tile = smem + (kv ? L::V_OFF : L::K_OFF) + s * L::TILE;
-        const uint8_t* raw = tile + (D / 64 - 1) * L::BLOCK + half * 8192;
-        const bool ok = (bars->half_ok[kv][s] >> half) & 1;
-        uint4 x[2][NC];
-        uint32_t pr[2];
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars->raw_full[rs], rph & 1, p.err))) return;
+      if (!__all_sync(0xffffffffu, mbar_wait(kv ? &bars->v_empty[s] : &bars->k_empty[s],
+                                             ((it / NSTAGE) & 1) ^ 1, p.err)))
+        return;
+      uint8_t* tile = smem + (kv ? L::V_OFF : L::K_OFF) + s * L::TILE;
+      const uint8_t* raw = smem + L::O_OFF + (rs * 2 + half) * i4_block_bytes(64, D);
+      const bool ok = (bars->half_ok[rs] >> half) & 1;
+      // a small loop (the kernel's roles share the instruction cache: unrolled over the rows and chunks it
+      // cost the whole kernel 26%), the next chunk's read in flight
+      uint4 nx = *reinterpret_cast<const uint4*>(raw + lane * (D / 2));
+      __nv_bfloat162 step, lo;
+#pragma unroll 1
+      for (int n = 0; n < 2 * NC; ++n) {
+        const int c = n & (NC - 1), r = lane + (n >= NC ? 32 : 0), rw = 64 * half + r;
+        const bool live = ok && kb + r <= G.kmax && (!MOD || kb + r >= G.kmin);
+        if (c == 0) i4_pair_bf162(live ? reinterpret_cast<const uint32_t*>(raw + 64 * (D / 2))[r] : 0u, step, lo);
+        const uint32_t w[4] = {live ? nx.x : 0u, live ? nx.y : 0u, live ? nx.z : 0u, live ? nx.w : 0u};
+        const int n2 = n + 1 < 2 * NC ? n + 1 : 0;
+        nx = *reinterpret_cast<const uint4*>(raw + (lane + (n2 >= NC ? 32 : 0)) * (D / 2) + (n2 & (NC - 1)) * 16);
+        uint8_t* dst = tile + (c >> 1) * L::BLOCK + rw * 128;
+        const uint32_t x = ((rw & 7) << 4) ^ ((c & 1) << 6);
 #pragma unroll
-        for (int rr = 0; rr < 2; ++rr) {
-          const int r = lane + 32 * rr;
-          const bool live = ok && kb + r <= G.kmax && (!MOD || kb + r >= G.kmin);
-#pragma unroll
-          for (int c = 0; c < NC; ++c)
-            x[rr][c] = live ? reinterpret_cast<const uint4*>(raw + r * (D / 2))[c] : make_uint4(0, 0, 0, 0);
-          pr[rr] = live ? reinterpret_cast<const uint32_t*>(raw + 64 * (D / 2))[r] : 0u;
-        }
-        __syncwarp();
-#pragma unroll
-        for (int rr = 0; rr < 2; ++rr) {
-          const int r = 64 * half + lane + 32 * rr;
-          __nv_bfloat162 step, lo;
-          i4_pair_bf162(pr[rr], step, lo);
-#pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            const uint32_t w[4] = {x[rr][c].x, x[rr][c].y, x[rr][c].z, x[rr][c].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int cc = 4 * c + i;
-              *reinterpret_cast<uint4*>(tile + (cc >> 3) * L::BLOCK + r * 128 + (((cc & 7) ^ (r & 7)) << 4)) =
-                  i4x8_bf16(w[i], step, lo);
-            }
-          }
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(kv ? &bars->v_full[s] : &bars->k_full[s]);
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(dst + (x ^ (i << 4))) = i4x8_bf16_perm(w[i], step, lo);
       }
+      fence_proxy_async_smem();
+      mbar_arrive(kv ? &bars->v_full[s] : &bars->k_full[s]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->raw_empty[rs]);
     }
   }
+}
+
+// The raw page blocks of a unit's tiles (4-bit pool, full layer), one warp. it: tiles copied so far.
+template <int D, bool MOD>
+__device__ bool raw_producer_i4(const Params& p, const Geo& G, uint8_t* smem, Bars* bars, uint32_t& it) {
+  using L = Layout<D>;
+  constexpr uint32_t BLK = (uint32_t)i4_block_bytes(64, D);
+  const int lane = threadIdx.x & 31;
+  for (int j = G.jb; j <= G.je; ++j, ++it) {
+    // the tile's two pages (lanes 0 and 1)
+    int page = -1;
+    {
+      const int lp = 2 * j + (lane & 1);
+      if (lp * 64 <= G.kmax && (!MOD || lp * 64 + 63 >= G.kmin)) {
+        page = lp < p.pt_stride ? p.page_table[(int64_t)G.b * p.pt_stride + lp] : -1;
+        if (page < 0 || page >= p.pages) {
+          if (lane < 2) record_error(p.err, HSWA_ERR_DEVICE_BOUNDS);
+          page = -1;
+        }
+      }
+    }
+    const int pg[2] = {__shfl_sync(0xffffffffu, page, 0), __shfl_sync(0xffffffffu, page, 1)};
+    const uint32_t ok = (pg[0] >= 0 ? 1u : 0u) | (pg[1] >= 0 ? 2u : 0u);
+    for (int kv = 0; kv < 2; ++kv) {
+      const int rs = kv ? NRAWK : it % NRAWK;
+      const uint32_t rph = kv ? it : it / NRAWK;
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars->raw_empty[rs], (rph & 1) ^ 1, p.err))) return false;
+      if (lane == 0) {
+        bars->half_ok[rs] = ok;
+        mbar_arrive_expect_tx(&bars->raw_full[rs], __popc(ok) * BLK);
+        for (int half = 0; half < 2; ++half)
+          if ((ok >> half) & 1)
+            bulk_load(smem + L::O_OFF + (rs * 2 + half) * BLK,
+                      (kv ? p.page_v8 : p.page_k8) +
+                          (((int64_t)p.full_layer * p.pages + pg[half]) * p.Hkv + G.g) * BLK,
+                      BLK, &bars->raw_full[rs]);
+      }
+      __syncwarp();
+    }
+  }
+  return true;
 }
 
 template <int D, bool I4, bool MOD>
@@ -552,6 +614,7 @@ __device__ void producer(const Params& p, uint8_t* smem, Bars* bars, const CUten
   const int lane = threadIdx.x & 31;
   int it = 0;        // K/V tiles loaded so far (stage ring position)
   uint32_t uq = 0;   // units started (Q buffer phase)
+  uint32_t rt = 0;   // raw page tiles copied (4-bit pages)
   uint32_t nfix = 0; // page tiles zero-filled past the last key (v_fix phase)
   for (int rnd = 0, unit = cta_unit(0); unit < p.n_units; unit = cta_unit(++rnd), ++uq) {
     Geo G;
@@ -575,6 +638,12 @@ __device__ void producer(const Params& p, uint8_t* smem, Bars* bars, const CUten
     const int seq = (!p.is_full && p.seq_ids) ? p.seq_ids[G.b] : 0;
     const bool ring_fast = p.ring_tma && (G.P % BN) == 0;
 
+    if constexpr (I4) {
+      if (p.is_full) {
+        if (!raw_producer_i4<D, MOD>(p, G, smem, bars, rt)) return;
+        continue;
+      }
+    }
     for (int j = G.jb; j <= G.je; ++j, ++it) {
       const int s = it % NSTAGE;
       const uint32_t ph = (it / NSTAGE) & 1;
@@ -584,36 +653,6 @@ __device__ void producer(const Params& p, uint8_t* smem, Bars* bars, const CUten
         uint64_t* empty = kv ? &bars->v_empty[s] : &bars->k_empty[s];
         uint8_t* dst = smem + (kv ? L::V_OFF : L::K_OFF) + s * L::TILE;
         if (!mbar_wait(empty, ph ^ 1, p.err)) return;
-        if constexpr (I4) {
-          if (p.is_full) {
-            uint64_t* raw = kv ? &bars->raw_v[s] : &bars->raw_k[s];
-            if (lane == 0) {
-              int64_t blk[2];
-              uint32_t ok = 0;
-              for (int half = 0; half < 2; ++half) {
-                const int pos0 = kb + 64 * half;
-                const int lp = pos0 / 64;
-                if (pos0 > kmax || (MOD && pos0 + 63 < kmin)) continue;
-                const int32_t page = lp < p.pt_stride ? p.page_table[(int64_t)G.b * p.pt_stride + lp] : -1;
-                if (page < 0 || page >= p.pages) {
-                  record_error(p.err, HSWA_ERR_DEVICE_BOUNDS);
-                } else {
-                  blk[half] = ((int64_t)p.full_layer * p.pages + page) * p.Hkv + G.g;
-                  ok |= 1u << half;
-                }
-              }
-              bars->half_ok[kv][s] = ok;
-              mbar_arrive_expect_tx(raw, __popc(ok) * (uint32_t)i4_block_bytes(64, D));
-              for (int half = 0; half < 2; ++half)
-                if ((ok >> half) & 1)
-                  bulk_load(dst + (D / 64 - 1) * L::BLOCK + half * 8192,
-                            (kv ? p.page_v8 : p.page_k8) + blk[half] * i4_block_bytes(64, D),
-                            (uint32_t)i4_block_bytes(64, D), raw);
-            }
-            __syncwarp();
-            continue;
-          }
-        }
         if (p.is_full && p.conv) {
           // FP8 pages: the codes go to the upper half of the stage buffer; page_converter makes bf16
           uint64_t* raw = kv ? &bars->raw_v[s] : &bars->raw_k[s];
@@ -727,7 +766,7 @@ __device__ void producer(const Params& p, uint8_t* smem, Bars* bars, const CUten
 
 // ---------------------------------------------------------------- MMA issuer
 
-template <int D, bool MOD>
+template <int D, bool I4, bool MOD>
 __device__ void mma_issuer(const Params& p, uint8_t* smem, Bars* bars, uint32_t tbase) {
   using L = Layout<D>;
   constexpr uint32_t IDESC_S = idesc_bf16_f32(BM, BN, false);
@@ -742,7 +781,7 @@ __device__ void mma_issuer(const Params& p, uint8_t* smem, Bars* bars, uint32_t 
   for (int rnd = 0, unit = cta_unit(0); unit < p.n_units; unit = cta_unit(++rnd), ++uq) {
     Geo G;
     make_geo<MOD>(p, unit, G);
-    if (!mbar_wait(&bars->q_full, uq & 1, p.err)) return;
+    if (!mbar_wait(I4 && p.is_full ? &bars->q_ready : &bars->q_full, uq & 1, p.err)) return;
     tc_fence_after();
 
     bool pend[NQT] = {false, false};
@@ -828,7 +867,7 @@ __device__ void mma_issuer(const Params& p, uint8_t* smem, Bars* bars, uint32_t 
 
 // ---------------------------------------------------------------- softmax + epilogue
 
-template <int D, bool MOD>
+template <int D, bool I4, bool MOD>
 __device__ void softmax_wg(const Params& p, uint8_t* smem, Bars* bars, uint32_t tbase, const int q,
                            const CUtensorMap* tm_o) {
   using L = Layout<D>;
@@ -886,7 +925,7 @@ __device__ void softmax_wg(const Params& p, uint8_t* smem, Bars* bars, uint32_t 
       const bool edge = !(kb + BN <= hi_first && kb >= lo_last);
       const int c_lo = lo_i - kb;
       const int c_hi = hi_i - kb;
-      if constexpr (MOD)
+      if (MOD && (p.sp.softcap > 0.f || p.sp.slope))  // with key ranges alone the scores are plain
         softmax_tile<D, 1, true>(trow, s_col, o_col, sl2, edge, c_lo, c_hi, m_used, l, n_done > 0, 0, false, &p.sp,
                                  slope2, (float)(i - kb));
       else
@@ -904,7 +943,12 @@ __device__ void softmax_wg(const Params& p, uint8_t* smem, Bars* bars, uint32_t 
       ++no;
     }
     tc_fence_after();
-    store_output<D, MOD>(trow, o_col, l, smem + L::O_OFF + q * L::BLOCK + wq * 4096, lane, tm_o, q ? G.hq[1] : G.hq[0],
+    if (I4 && p.is_full)
+      store_output_direct<D>(trow, o_col, l,
+                             p.o + (((int64_t)G.b * p.n_q + qt * BM + r) * p.Hq + (q ? G.hq[1] : G.hq[0])) * D,
+                             qt * BM + r < p.n_q);
+    else
+      store_output<D, MOD>(trow, o_col, l, smem + L::O_OFF + q * L::BLOCK + wq * 4096, lane, tm_o, q ? G.hq[1] : G.hq[0],
                     qt * BM + wq * 32, G.b, p.n_q);
     // O of this query tile has been read: the next unit's first P V may overwrite it
     // (ordered by this warpgroup's next p_full arrival).
@@ -913,7 +957,7 @@ __device__ void softmax_wg(const Params& p, uint8_t* smem, Bars* bars, uint32_t 
 }
 
 template <int D, bool I4, bool MOD>
-__global__ void __launch_bounds__(NTHREADS, 1)
+__global__ void __launch_bounds__(I4 ? NTHREADS_I4 : NTHREADS, 1)
     prefill_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tm_q,
                    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                    const __grid_constant__ CUtensorMap tm_rk, const __grid_constant__ CUtensorMap tm_rv,
@@ -929,6 +973,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   if (threadIdx.x == 0) {
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, 1);
+    mbar_init(&bars->q_ready, 128);
     for (int s = 0; s < NSTAGE; ++s) {
       mbar_init(&bars->k_full[s], p.conv ? 64 : 1);  // converting threads, or the loading thread
       mbar_init(&bars->v_full[s], p.conv ? 64 : 1);
@@ -941,6 +986,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       mbar_init(&bars->s_full[q], 1);
       mbar_init(&bars->p_full[q], 128);
       mbar_init(&bars->o_full[q], 1);
+    }
+    for (int i = 0; i < NRAW; ++i) {
+      mbar_init(&bars->raw_full[i], 1);
+      mbar_init(&bars->raw_empty[i], 2);  // the two converting warps
     }
     mbar_init(&bars->v_fix, 1);
     fence_barrier_init();
@@ -962,19 +1011,26 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 
   if (warp < 8) {
     // two softmax warpgroups take the registers the third one gives back
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 " HSWA_STR(HSWA_SOFTMAX_REGS) ";" ::: "memory");
-    softmax_wg<D, MOD>(p, smem, bars, tbase, warp >> 2, &tm_o);
+    if constexpr (I4)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 " HSWA_STR(HSWA_SOFTMAX_REGS_I4) ";" ::: "memory");
+    else
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 " HSWA_STR(HSWA_SOFTMAX_REGS) ";" ::: "memory");
+    softmax_wg<D, I4, MOD>(p, smem, bars, tbase, warp >> 2, &tm_o);
     if ((threadIdx.x & 31) == 0) bulk_wait_all();  // output stores complete before the CTA exits
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 " HSWA_STR(HSWA_PRODUCER_REGS) ";" ::: "memory");
+    if constexpr (I4)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 " HSWA_STR(HSWA_PRODUCER_REGS_I4) ";" ::: "memory");
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 " HSWA_STR(HSWA_PRODUCER_REGS) ";" ::: "memory");
     if (warp == PRODUCER_WARP) {
       producer<D, I4, MOD>(p, smem, bars, &tm_q, &tm_k, &tm_v, &tm_rk, &tm_rv);
     } else if (warp == MMA_WARP) {
-      if ((threadIdx.x & 31) == 0) mma_issuer<D, MOD>(p, smem, bars, tbase);
+      if ((threadIdx.x & 31) == 0) mma_issuer<D, I4, MOD>(p, smem, bars, tbase);
       __syncwarp();
     } else if (p.conv) {
-      if constexpr (I4) page_converter_i4<D, MOD>(p, smem, bars);
-      else if constexpr (D == 128) page_converter<D, MOD>(p, smem, bars);
+      if constexpr (I4) {
+        if (warp >= NWARPS) page_converter_i4<D, MOD>(p, smem, bars, (warp - NWARPS) >> 1, warp & 1);
+      } else if constexpr (D == 128) page_converter<D, MOD>(p, smem, bars);
     }
   }
 
@@ -1006,6 +1062,7 @@ int launch_prefill(const PrefillLaunch& Lc, cudaStream_t stream) {
   p.seq_ids = Lc.seq_ids;
   p.page_table = Lc.page_table;
   p.pt_stride = Lc.pt_stride;
+  p.o = Lc.o;
   p.ring_k = pool->ring_k;
   p.ring_v = pool->ring_v;
   p.ring_k8 = pool->ring_k8;
@@ -1069,7 +1126,7 @@ int launch_prefill(const PrefillLaunch& Lc, cudaStream_t stream) {
 #define HSWA_PREFILL(DD, I4_, MOD_)                                                                                 \
   do {                                                                                                               \
     cudaFuncSetAttribute(prefill_kernel<DD, I4_, MOD_>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);          \
-    prefill_kernel<DD, I4_, MOD_><<<grid, NTHREADS, smem, stream>>>(p, Lc.tm_q, Lc.tm_k, Lc.tm_v, rk, rv, Lc.tm_o);  \
+    prefill_kernel<DD, I4_, MOD_><<<grid, I4_ ? NTHREADS_I4 : NTHREADS, smem, stream>>>(p, Lc.tm_q, Lc.tm_k, Lc.tm_v, rk, rv, Lc.tm_o);  \
   } while (0)
 #define HSWA_PREFILL_D(DD)                                \
   do {                                                    \

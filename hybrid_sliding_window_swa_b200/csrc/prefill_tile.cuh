@@ -54,6 +54,8 @@ struct ScoreParams {
   float cap_in, cap_log2;  // 2 log2(e) scale / cap, cap log2 e
   float poly_max;          // raw scores up to this magnitude take the polynomial (0: none do)
   float poly[6];           // cap log2(e) tanh(x scale / cap) = x (poly[0] + poly[1] x^2 + ...)
+  float near_max;          // the same with three terms for |x| up to near_max = 0.35 cap / scale
+  float near[3];
   const float* slope;      // [Hq] distance slopes, or null
   const int64_t* key_begin;  // [B][n_q], or null
   const int64_t* key_end;
@@ -76,8 +78,14 @@ inline void fill_score_params(const hswa_score_mod& m, double scale, ScoreParams
                          -0.05158598840417456, 0.01672085517953942, -0.0030582290375864097};
     if (c1 >= 6e-4 && c1 <= 100.0) {
       sp->poly_max = (float)(1.0 / c1);
+      // three terms on |u| <= 0.35, off by at most 1e-6
+      const double N[3] = {0.9999971183259196, -0.3329087359461866, 0.12394375936961438};
+      sp->near_max = (float)(0.35 / c1);
       double f = log2e * m.softcap * c1;
-      for (int i = 0; i < 6; ++i, f *= c1 * c1) sp->poly[i] = (float)(T[i] * f);
+      for (int i = 0; i < 6; ++i, f *= c1 * c1) {
+        sp->poly[i] = (float)(T[i] * f);
+        if (i < 3) sp->near[i] = (float)(N[i] * f);
+      }
     }
   }
 }
@@ -86,20 +94,12 @@ inline void fill_score_params(const hswa_score_mod& m, double scale, ScoreParams
 // column (its position minus the tile's), so column k is |c_q - k| away.
 // The cap costs what tanh costs: through exponential and reciprocal it is two more MUFU operations per
 // score, on the unit that the softmax itself loads most. While every score of the warp stays within the
-// cap (|s| <= cap, the usual case), the degree-11 polynomial on the FMA pipe replaces them: 7 packed
-// multiply-adds per pair.
+// cap (|s| <= cap), the degree-11 polynomial on the FMA pipe replaces them: 7 packed multiply-adds per pair.
+// Bias: on a tile wholly before the warp's queries |c_q - k| = c_q - k, two packed operations per pair.
 __device__ __forceinline__ void modify_scores(uint32_t (&v)[128], const ScoreParams& sp, float sl2, float slope2,
-                                              float c_q) {
+                                              float c_q, float abs_max) {
   if (sp.softcap > 0.f) {
-    float m0 = 0.f, m1 = 0.f, m2 = 0.f, m3 = 0.f;
-#pragma unroll
-    for (int k = 0; k < 128; k += 8) {
-      m0 = fmax3(m0, fabsf(__uint_as_float(v[k])), fabsf(__uint_as_float(v[k + 1])));
-      m1 = fmax3(m1, fabsf(__uint_as_float(v[k + 2])), fabsf(__uint_as_float(v[k + 3])));
-      m2 = fmax3(m2, fabsf(__uint_as_float(v[k + 4])), fabsf(__uint_as_float(v[k + 5])));
-      m3 = fmax3(m3, fabsf(__uint_as_float(v[k + 6])), fabsf(__uint_as_float(v[k + 7])));
-    }
-    if (__all_sync(0xffffffffu, fmaxf(fmax3(m0, m1, m2), m3) <= sp.poly_max)) {
+    if (__all_sync(0xffffffffu, abs_max <= sp.poly_max)) {
       uint64_t c[6];
 #pragma unroll
       for (int i = 0; i < 6; ++i) c[i] = f2_pack(sp.poly[i], sp.poly[i]);
@@ -123,20 +123,26 @@ __device__ __forceinline__ void modify_scores(uint32_t (&v)[128], const ScorePar
       for (int k = 0; k < 128; ++k)
         v[k] = __float_as_uint(capped_log2(__uint_as_float(v[k]), sp.cap_in, sp.cap_log2));
     }
-  } else {
-    const uint64_t s2 = f2_pack(sl2, sl2);
-#pragma unroll
-    for (int k = 0; k < 128; k += 2) {
-      float a, b;
-      f2_unpack(f2_mul(f2_pack(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), s2), a, b);
-      v[k] = __float_as_uint(a);
-      v[k + 1] = __float_as_uint(b);
-    }
+    sl2 = 1.f;
   }
   if (sp.slope) {
+    if (__all_sync(0xffffffffu, c_q >= 127.f)) {
+      // x sl2 + slope2 (k - c_q), k - c_q exact
+      const uint64_t s2 = f2_pack(sl2, sl2), b2 = f2_pack(slope2, slope2), two = f2_pack(2.f, 2.f);
+      uint64_t d = f2_pack(-c_q, 1.f - c_q);
 #pragma unroll
-    for (int k = 0; k < 128; ++k)
-      v[k] = __float_as_uint(fmaf(-slope2, fabsf(c_q - (float)k), __uint_as_float(v[k])));
+      for (int k = 0; k < 128; k += 2) {
+        float a, b;
+        f2_unpack(f2_fma(f2_pack(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), s2, f2_mul(d, b2)), a, b);
+        v[k] = __float_as_uint(a);
+        v[k + 1] = __float_as_uint(b);
+        d = f2_add(d, two);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 128; ++k)
+        v[k] = __float_as_uint(fmaf(-slope2, fabsf(c_q - (float)k), __uint_as_float(v[k]) * sl2));
+    }
   }
 }
 
@@ -177,9 +183,29 @@ __device__ __forceinline__ void softmax_tile(uint32_t trow, uint32_t s_col, uint
     reg_fence_into<32>(v);
     reg_fence_into<64>(v);
     reg_fence_into<96>(v);
+    // MOD: `near` = capped scores without a bias, all of the warp's within 0.35 cap. The cap is monotone,
+    // so the row maximum is taken on raw scores and capped alone, and the three-term polynomial goes into
+    // the exponential's argument: 3 packed operations per pair. (Masked scores, -inf, come out as -inf:
+    // the polynomial's highest coefficient is positive.)
+    bool near = false;
     if constexpr (MOD) {
-      modify_scores(v, *sp, sl2, slope2, c_q);
-      sl2 = 1.f;
+      float am = 0.f;
+      if (sp->softcap > 0.f) {
+        float m0 = 0.f, m1 = 0.f, m2 = 0.f, m3 = 0.f;
+#pragma unroll
+        for (int k = 0; k < 128; k += 8) {
+          m0 = fmax3(m0, fabsf(__uint_as_float(v[k])), fabsf(__uint_as_float(v[k + 1])));
+          m1 = fmax3(m1, fabsf(__uint_as_float(v[k + 2])), fabsf(__uint_as_float(v[k + 3])));
+          m2 = fmax3(m2, fabsf(__uint_as_float(v[k + 4])), fabsf(__uint_as_float(v[k + 5])));
+          m3 = fmax3(m3, fabsf(__uint_as_float(v[k + 6])), fabsf(__uint_as_float(v[k + 7])));
+        }
+        am = fmaxf(fmax3(m0, m1, m2), m3);
+        near = __all_sync(0xffffffffu, am <= sp->near_max) && !sp->slope;
+      }
+      if (!near) {
+        modify_scores(v, *sp, sl2, slope2, c_q, am);
+        sl2 = 1.f;
+      }
     }
     if (MASK_MODE == 2) {
       // block 0 = chunk rot: the lower edge keeps j > lane, the diagonal keeps j <= lane
@@ -229,7 +255,10 @@ __device__ __forceinline__ void softmax_tile(uint32_t trow, uint32_t s_col, uint
     m0 = fmax3(m0, __uint_as_float(v[124]), __uint_as_float(v[125]));
     m1 = fmax3(m1, __uint_as_float(v[126]), __uint_as_float(v[127]));
     const float mx = fmaxf(fmax3(m0, m1, m2), m3);
-    const float m_tile = mx * sl2;
+    float m_tile = mx * sl2;
+    if constexpr (MOD) {
+      if (near) m_tile = mx == -INFINITY ? mx : mx * fmaf(fmaf(sp->near[2], mx * mx, sp->near[1]), mx * mx, sp->near[0]);
+    }
     float alpha = 1.f;
     bool resc = false;
     if (m_tile > m_used + kTau) {
@@ -252,6 +281,37 @@ __device__ __forceinline__ void softmax_tile(uint32_t trow, uint32_t s_col, uint
         tmem_st32(trow + o_col + c0, o);
       }
       tmem_wait_st();
+    }
+    if constexpr (MOD) {
+      if (near) {
+        const float mo = (m_used == -INFINITY) ? 0.f : m_used;
+        const uint64_t n0 = f2_pack(sp->near[0], sp->near[0]), n1 = f2_pack(sp->near[1], sp->near[1]),
+                       n2 = f2_pack(sp->near[2], sp->near[2]), neg = f2_pack(-mo, -mo);
+        uint64_t ac[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int c0 = 0; c0 < BN; c0 += 32) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            const uint64_t x = f2_pack(__uint_as_float(v[c0 + k]), __uint_as_float(v[c0 + k + 1]));
+            const uint64_t t = f2_mul(x, x);
+            float e0, e1;
+            f2_unpack(f2_fma(x, f2_fma(f2_fma(n2, t, n1), t, n0), neg), e0, e1);
+            e0 = ex2_approx(e0);
+            e1 = ex2_approx(e1);
+            ac[(k >> 1) & 3] = f2_add(ac[(k >> 1) & 3], f2_pack(e0, e1));
+            pk[k >> 1] = pack_bf16x2(e0, e1);
+          }
+          tmem_st16(trow + s_col + 16 * (c0 >> 5), pk);
+        }
+        float a0, a1, b0, b1, d0, d1, f0, f1;
+        f2_unpack(ac[0], a0, a1);
+        f2_unpack(ac[1], b0, b1);
+        f2_unpack(ac[2], d0, d1);
+        f2_unpack(ac[3], f0, f1);
+        l += ((a0 + a1) + (b0 + b1)) + ((d0 + d1) + (f0 + f1));
+        return;
+      }
     }
     // P = 2^(s * scale * log2 e - m) in place, packed to bf16 and stored over S
     const float moff = (m_used == -INFINITY) ? 0.f : m_used;
@@ -441,6 +501,33 @@ __device__ __forceinline__ void store_output(uint32_t trow, uint32_t o_col, floa
   }
 }
 
+// The epilogue without staging: each thread writes its row's O / l (zeros when l = 0) with 16-byte stores.
+// The columns of every group of eight hold the dims 0 4 1 5 2 6 3 7 (i4x8_bf16_perm).
+template <int D>
+__device__ __forceinline__ void store_output_direct(uint32_t trow, uint32_t o_col, float l, uint16_t* row, bool live) {
+  const float inv = 1.f / l;
+  const bool none = l == 0.f;
+#pragma unroll
+  for (int c0 = 0; c0 < D; c0 += 32) {
+    uint32_t o[32];
+    tmem_ld32(trow + o_col + c0, o);
+    tmem_wait_ld();
+    reg_fence32(o);
+    uint32_t pk[16];
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) {
+      // dims k, k + 1 of a group of eight are 0 2 | 4 6 | 1 3 | 5 7
+      const int c = (k & ~7) + ((k & 2) << 1) + ((k & 4) >> 2);
+      pk[k >> 1] = none ? 0u : pack_bf16x2(__uint_as_float(o[c]) * inv, __uint_as_float(o[c + 2]) * inv);
+    }
+    if (live) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        reinterpret_cast<uint4*>(row + c0)[x] = make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
+    }
+  }
+}
+
 // store_output for a caller whose next MMA waits for O's TMEM columns: all D columns of the row
 // are read into registers first, `o_free` gets this thread's arrival (the columns may be
 // overwritten from then on), and the packing, staging and TMA stores follow.
@@ -585,6 +672,19 @@ __device__ __forceinline__ uint4 i4x8_bf16(uint32_t w, __nv_bfloat162 step, __nv
   for (int i = 0; i < 4; ++i) {
     const uint32_t z = (w >> (8 * i)) & 0xFFu;
     const uint32_t pair = ((z * 0x1001u) & 0x000F000Fu) | 0x43004300u;
+    const __nv_bfloat162 c = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&pair), __nv_bfloat162(128.f, 128.f));
+    const __nv_bfloat162 y = __hfma2(c, step, lo);
+    o[i] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// The same with the eight dims in the order 0 4 1 5 2 6 3 7, as one mask takes them from the word.
+__device__ __forceinline__ uint4 i4x8_bf16_perm(uint32_t w, __nv_bfloat162 step, __nv_bfloat162 lo) {
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t pair = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
     const __nv_bfloat162 c = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&pair), __nv_bfloat162(128.f, 128.f));
     const __nv_bfloat162 y = __hfma2(c, step, lo);
     o[i] = *reinterpret_cast<const uint32_t*>(&y);
