@@ -69,82 +69,119 @@ __device__ __forceinline__ void rotate_unit(uint4& A, uint4& B, const float* cs,
 template <int D, int FMT>
 __global__ void __launch_bounds__(RT) rope_kernel(const __grid_constant__ RopeParams p, int tpb) {
   constexpr int UPR = D / 16;  // units per row
-  __shared__ float cs[8 * 64], sn[8 * 64];
+  __shared__ float cs[4 * 64], sn[4 * 64];
   const int64_t n0 = (int64_t)blockIdx.x * tpb;
   const int nt = (int)min((int64_t)tpb, p.n - n0);
+  // a thread keeps its unit of the row (and so its chunks and frequencies) and walks rows (token, head),
+  // two at a time, the next two being read while these are turned; the first two are on their way while
+  // the table is made
+  const int heads = p.Hq + p.Hkv + (FMT ? p.Hkv : 0);
+  const int total = nt * heads;
+  const bool pairs = p.interleaved != 0;
+  const int u = threadIdx.x % UPR;
+  const bool rotated = u < (p.rot >> 4);
+  const int c0 = rotated && !pairs ? u : 2 * u;
+  const int c1 = rotated && !pairs ? u + (p.rot >> 4) : 2 * u + 1;
+  const unsigned group = ((1u << UPR) - 1u) << ((threadIdx.x & 31) & ~(UPR - 1));
+  constexpr int STEP = RT / UPR;
+  constexpr int BATCH = 2;
+  int t = 0, h = threadIdx.x / UPR;  // of the next row to read
+  uint4 nA[BATCH], nB[BATCH];
+  int nt_[BATCH], nh[BATCH];
+  auto read = [&](int r) {
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      while (h >= heads) {
+        h -= heads;
+        ++t;
+      }
+      nt_[k] = t;
+      nh[k] = h;
+      if (r + k * STEP < total) {
+        const int64_t n = n0 + t;
+        const uint16_t* src = h < p.Hq ? p.q + (n * p.Hq + h) * D
+                              : h < p.Hq + p.Hkv ? p.k + (n * p.Hkv + (h - p.Hq)) * D
+                                                 : p.v + (n * p.Hkv + (h - p.Hq - p.Hkv)) * D;
+        nA[k] = reinterpret_cast<const uint4*>(src)[c0];
+        nB[k] = reinterpret_cast<const uint4*>(src)[c1];
+      }
+      h += STEP;
+    }
+  };
+  read(threadIdx.x / UPR);
   const int half = p.rot >> 1;
   for (int i = threadIdx.x; i < nt * half; i += RT) {
-    const int t = i / half, f = i - t * half;
-    const double turns = (double)p.pos[(int64_t)p.axis[f] * p.n + n0 + t] * p.turns[f];
+    const int tk = i / half, f = i - tk * half;
+    const double turns = (double)p.pos[(int64_t)p.axis[f] * p.n + n0 + tk] * p.turns[f];
     const float frac = (float)(turns - rint(turns));  // in [-1/2, 1/2]
     float s, c;
     sincospif(2.f * frac, &s, &c);
-    cs[t * 64 + f] = c;
-    sn[t * 64 + f] = s;
+    cs[tk * 64 + f] = c;
+    sn[tk * 64 + f] = s;
   }
   __syncthreads();
-  const int heads = p.Hq + p.Hkv + (FMT ? p.Hkv : 0);
-  const int total = nt * heads * UPR;
-  const unsigned group = ((1u << UPR) - 1u) << ((threadIdx.x & 31) & ~(UPR - 1));
-  const bool pairs = p.interleaved != 0;
-#pragma unroll 2
-  for (int i = threadIdx.x; i < total; i += RT) {
-    const int u = i % UPR;
-    const int r = i / UPR;
-    const int t = r / heads, h = r - t * heads;
-    const int64_t n = n0 + t;
-    const bool rotated = u < (p.rot >> 4);
-    const int c0 = rotated && !pairs ? u : 2 * u;
-    const int c1 = rotated && !pairs ? u + (p.rot >> 4) : 2 * u + 1;
-    const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hkv;
-    const int g = is_q ? 0 : (is_k ? h - p.Hq : h - p.Hq - p.Hkv);
-    const int64_t off = (is_q ? n * p.Hq + h : n * p.Hkv + g) * D;
-    const uint4* src = reinterpret_cast<const uint4*>((is_q ? p.q : is_k ? p.k : p.v) + off);
-    uint4 A = src[c0], B = src[c1];
-    if (rotated && (is_q || is_k)) rotate_unit(A, B, cs + t * 64 + 8 * u, sn + t * 64 + 8 * u, pairs);
-    uint16_t* out = is_q ? p.q_out : is_k ? p.k_out : nullptr;
-    if (out) {
-      reinterpret_cast<uint4*>(out + off)[c0] = A;
-      reinterpret_cast<uint4*>(out + off)[c1] = B;
-    }
-    if constexpr (FMT != 0) {
-      if (is_q) continue;
-      const int b = (int)(n / p.dst.n_tok), tt = (int)(n - (int64_t)b * p.dst.n_tok);
-      int64_t block, row;
-      if (!commit_place(p.dst, b, tt, g, block, row)) continue;  // the same for the whole row
-      const int64_t rows = p.dst.is_swa ? p.dst.W : 64;
-      uint8_t* base = is_k ? p.dst.k : p.dst.v;
-      if constexpr (FMT == 1) {
-        uint4* d = reinterpret_cast<uint4*>(base + (block * rows + row) * D * 2);
-        d[c0] = A;
-        d[c1] = B;
-      } else if constexpr (FMT == 2) {
-        const float inv = (is_k ? p.dst.inv_k : p.dst.inv_v)[g];
-        uint2* d = reinterpret_cast<uint2*>(base + (block * rows + row) * D);
-        auto q8 = [inv](const uint4& x) {
-          return make_uint2((uint32_t)pack_e4m3x2(bf_lo(x.x) * inv, bf_hi(x.x) * inv) |
-                                ((uint32_t)pack_e4m3x2(bf_lo(x.y) * inv, bf_hi(x.y) * inv) << 16),
-                            (uint32_t)pack_e4m3x2(bf_lo(x.z) * inv, bf_hi(x.z) * inv) |
-                                ((uint32_t)pack_e4m3x2(bf_lo(x.w) * inv, bf_hi(x.w) * inv) << 16));
-        };
-        d[c0] = q8(A);
-        d[c1] = q8(B);
-      } else {
-        const uint32_t a[4] = {A.x, A.y, A.z, A.w}, bb[4] = {B.x, B.y, B.z, B.w};
-        RowRange rr;
+  for (int r = threadIdx.x / UPR; r < total; r += BATCH * STEP) {
+    uint4 A[BATCH], B[BATCH];
+    int tt[BATCH], hh[BATCH];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          rr.add(a[x]);
-          rr.add(bb[x]);
+    for (int k = 0; k < BATCH; ++k) {
+      A[k] = nA[k];
+      B[k] = nB[k];
+      tt[k] = nt_[k];
+      hh[k] = nh[k];
+    }
+    read(r + BATCH * STEP);
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      if (r + k * STEP >= total) break;  // the same for the whole row
+      const int64_t n = n0 + tt[k];
+      const bool is_q = hh[k] < p.Hq, is_k = !is_q && hh[k] < p.Hq + p.Hkv;
+      const int g = is_q ? 0 : (is_k ? hh[k] - p.Hq : hh[k] - p.Hq - p.Hkv);
+      if (rotated && (is_q || is_k)) rotate_unit(A[k], B[k], cs + tt[k] * 64 + 8 * u, sn + tt[k] * 64 + 8 * u, pairs);
+      uint16_t* out = is_q ? p.q_out + (n * p.Hq + hh[k]) * D : is_k && p.k_out ? p.k_out + (n * p.Hkv + g) * D : nullptr;
+      if (out) {
+        reinterpret_cast<uint4*>(out)[c0] = A[k];
+        reinterpret_cast<uint4*>(out)[c1] = B[k];
+      }
+      if constexpr (FMT != 0) {
+        if (is_q) continue;
+        const int b = (int)(n / p.dst.n_tok), tok = (int)(n - (int64_t)b * p.dst.n_tok);
+        int64_t block, row;
+        if (!commit_place(p.dst, b, tok, g, block, row)) continue;  // the same for the whole row
+        const int64_t rows = p.dst.is_swa ? p.dst.W : 64;
+        uint8_t* base = is_k ? p.dst.k : p.dst.v;
+        if constexpr (FMT == 1) {
+          uint4* d = reinterpret_cast<uint4*>(base + (block * rows + row) * D * 2);
+          d[c0] = A[k];
+          d[c1] = B[k];
+        } else if constexpr (FMT == 2) {
+          const float inv = (is_k ? p.dst.inv_k : p.dst.inv_v)[g];
+          uint2* d = reinterpret_cast<uint2*>(base + (block * rows + row) * D);
+          auto q8 = [inv](const uint4& x) {
+            return make_uint2((uint32_t)pack_e4m3x2(bf_lo(x.x) * inv, bf_hi(x.x) * inv) |
+                                  ((uint32_t)pack_e4m3x2(bf_lo(x.y) * inv, bf_hi(x.y) * inv) << 16),
+                              (uint32_t)pack_e4m3x2(bf_lo(x.z) * inv, bf_hi(x.z) * inv) |
+                                  ((uint32_t)pack_e4m3x2(bf_lo(x.w) * inv, bf_hi(x.w) * inv) << 16));
+          };
+          d[c0] = q8(A[k]);
+          d[c1] = q8(B[k]);
+        } else {
+          const uint32_t a[4] = {A[k].x, A[k].y, A[k].z, A[k].w}, bb[4] = {B[k].x, B[k].y, B[k].z, B[k].w};
+          RowRange rr;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            rr.add(a[x]);
+            rr.add(bb[x]);
+          }
+          rr.reduce<UPR>(group);
+          float inv;
+          const uint32_t pair = i4_params(rr.lo, rr.hi, rr.finite, inv);
+          uint8_t* blk = base + block * i4_block_bytes(rows, D);
+          uint32_t* d = reinterpret_cast<uint32_t*>(i4_codes<D>(blk, row));
+          d[c0] = i4_pack8(a, rr.lo, inv);
+          d[c1] = i4_pack8(bb, rr.lo, inv);
+          if (u == 0) *i4_pair<D>(blk, rows, row) = pair;
         }
-        rr.reduce<UPR>(group);
-        float inv;
-        const uint32_t pair = i4_params(rr.lo, rr.hi, rr.finite, inv);
-        uint8_t* blk = base + block * i4_block_bytes(rows, D);
-        uint32_t* d = reinterpret_cast<uint32_t*>(i4_codes<D>(blk, row));
-        d[c0] = i4_pack8(a, rr.lo, inv);
-        d[c1] = i4_pack8(bb, rr.lo, inv);
-        if (u == 0) *i4_pair<D>(blk, rows, row) = pair;
       }
     }
   }
