@@ -348,6 +348,8 @@ def rope_fwd(rope: RopeDesc, q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor
     d = qs[-1]
     if qs[:-2] != ks[:-2] or d != ks[-1]:
         raise ValueError("q and k must have the same tokens and head_dim")
+    if q.device.index != torch.cuda.current_device() or k.device != q.device or pos.device != q.device:
+        raise ValueError("q, k and pos must be on the current CUDA device")
     n = math.prod(qs[:-2])
     if pos.shape[0] != rope.n_axes or pos.numel() != rope.n_axes * n:
         raise ValueError(f"pos must be [n_axes, tokens] = [{rope.n_axes}, {n}], got {tuple(pos.shape)}")

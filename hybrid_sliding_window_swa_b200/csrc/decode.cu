@@ -494,13 +494,17 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) decode_kernel(DecParams p) {
     const int a = klo + c * split;
     const int b = (a + split < khi) ? a + split : khi;
     const int n_cached_blk = (b - a + KB - 1) / KB;
-    int lo_all = 0;  // EXT: rows of a page below every row's range are not read
+    int lo_all = 0, hi_all = 0x7fffffff;  // EXT: entries outside every row's range are not read
     if constexpr (EXT) {
       lo_all = 0x7fffffff;
+      hi_all = 0;
       for (int t = 0; t < p.n_qt; ++t) {
         int rl, rh;
         row_range(p, s, L, t, rl, rh);
-        if (rh > rl) lo_all = min(lo_all, rl);
+        if (rh > rl) {
+          lo_all = min(lo_all, rl);
+          hi_all = max(hi_all, rh);
+        }
       }
     }
     const int n_blk = n_cached_blk + (last ? 1 : 0);
@@ -587,7 +591,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) decode_kernel(DecParams p) {
         for (int rr = 0; rr < KB; rr += CP_ROWS) {
           const int r = rr + cp_row;
           uint4 qk = make_uint4(0, 0, 0, 0), qv = make_uint4(0, 0, 0, 0);
-          if (r < p.n_qt) {
+          if (r < p.n_qt && (!EXT || (L + r >= lo_all && L + r < hi_all))) {
             const int64_t row = ((int64_t)s * p.n_qt + r) * p.Hkv + g;
             qk = q16(p.k_new + row * D + cp_chunk * 16, ik);
             qv = q16(p.v_new + row * D + cp_chunk * 16, iv);
@@ -600,7 +604,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) decode_kernel(DecParams p) {
 #pragma unroll
         for (int rr = 0; rr < KB; rr += CP_ROWS) {
           const int r = rr + cp_row;
-          const bool ok = r < p.n_qt;
+          const bool ok = r < p.n_qt && (!EXT || (L + r >= lo_all && L + r < hi_all));
           const int64_t row = ((int64_t)s * p.n_qt + (ok ? r : 0)) * p.Hkv + g;
           const uint16_t* sk = p.k_new + row * D + cp_chunk * 8;
           const uint16_t* sv = p.v_new + row * D + cp_chunk * 8;
@@ -1363,6 +1367,23 @@ int launch_tc(DecParams& p, int n_items_max, int sms, size_t merge_smem, cudaStr
 }
 
 }  // namespace
+
+// What hybrid_decode_workspace_size promises for extended launches: at least the items of any call with at
+// most these sequences and this context length, and growing with both (the exact count need not: fewer
+// sequences may be cut finer).
+int64_t ext_items_bound(int n_seqs, int Hkv, int64_t max_ctx_len) {
+  const int64_t pairs = (int64_t)n_seqs * Hkv;
+  const int64_t coarse = pairs * max_splits(0, max_ctx_len, SPLIT), fine = pairs * max_splits(0, max_ctx_len, 2048);
+  const int64_t least = kExtCtas + pairs > fine ? kExtCtas + pairs : fine;
+  const int64_t cut = 4 * kExtCtas + pairs < least ? 4 * kExtCtas + pairs : least;
+  return coarse > cut ? coarse : cut;
+}
+
+size_t decode_workspace_bound(int n_seqs, int n_qt, int Hq, int Hkv, int d, int64_t max_ctx_len) {
+  WsLayout a(n_seqs, n_qt * (Hq / Hkv), d, (int64_t)n_seqs * Hkv * max_splits(0, max_ctx_len));
+  WsLayout b(n_seqs, n_qt * (Hq / Hkv), d, ext_items_bound(n_seqs, Hkv, max_ctx_len));
+  return a.bytes > b.bytes ? a.bytes : b.bytes;
+}
 
 int64_t decode_max_items(int n_seqs, int Hkv, int window, int64_t max_ctx_len, bool ext) {
   const int split = ext ? ext_split(n_seqs, Hkv, window, max_ctx_len) : SPLIT;

@@ -103,7 +103,7 @@ struct I4Item {
   int n_cached, n_blk;   // blocks of cached keys, blocks with the new tokens
   int nsp;               // splits of the sequence
   int lo_min, lo_max;    // over the rows: smallest and largest first visible position
-  int hi_min;            // smallest end of the visible range
+  int hi_min, hi_max;    // smallest and largest end of the visible ranges
   int row_lo[8], row_hi[8];  // per new token
 };
 
@@ -259,12 +259,14 @@ __global__ void __launch_bounds__(I4Cfg<NT>::THREADS, I4Cfg<NT>::CTAS) decode_i4
       // visible range of each new token's rows, by lane
       int rlo = 0, rhi = 0x7fffffff;
       row_range(p, s, L, lane < p.n_qt ? lane : 0, rlo, rhi);
-      int lo_min = rhi > rlo ? rlo : 0x7fffffff, lo_max = rlo, hi_min = rhi;  // a row may see nothing
+      // (a row may see nothing)
+      int lo_min = rhi > rlo ? rlo : 0x7fffffff, hi_max = rhi > rlo ? rhi : 0, lo_max = rlo, hi_min = rhi;
 #pragma unroll
       for (int x = 1; x < 8; x <<= 1) {
         lo_min = min(lo_min, __shfl_xor_sync(0xffffffffu, lo_min, x));
         lo_max = max(lo_max, __shfl_xor_sync(0xffffffffu, lo_max, x));
         hi_min = min(hi_min, __shfl_xor_sync(0xffffffffu, hi_min, x));
+        hi_max = max(hi_max, __shfl_xor_sync(0xffffffffu, hi_max, x));
       }
       if (lane < 8) {
         I.row_lo[lane] = rlo;
@@ -284,6 +286,7 @@ __global__ void __launch_bounds__(I4Cfg<NT>::THREADS, I4Cfg<NT>::CTAS) decode_i4
         I.lo_min = lo_min;
         I.lo_max = lo_max;
         I.hi_min = hi_min;
+        I.hi_max = hi_max;
         const uint32_t row_bytes = p.G * D * 2;
         mbar_arrive_expect_tx(&item_full[slot], p.n_qt * row_bytes);
         uint8_t* dst = smem + SM::Q_OFF + slot * SM::Q_BYTES;
@@ -504,7 +507,7 @@ __global__ void __launch_bounds__(I4Cfg<NT>::THREADS, I4Cfg<NT>::CTAS) decode_i4
     }
 
     float o[MT][NT][4];
-    float m[NT][2], l[NT][2], bs[NT][2];
+    float m[NT][2], l[NT][2], bs[NT][2], l_sh[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -512,6 +515,7 @@ __global__ void __launch_bounds__(I4Cfg<NT>::THREADS, I4Cfg<NT>::CTAS) decode_i4
         m[nt][c] = -INFINITY;
         l[nt][c] = 0.f;
         bs[nt][c] = 0.f;
+        l_sh[nt][c] = 0.f;
       }
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -520,7 +524,8 @@ __global__ void __launch_bounds__(I4Cfg<NT>::THREADS, I4Cfg<NT>::CTAS) decode_i4
     int e_cur = -120;        // V steps are used divided by 2^e_cur
     float fe = pow2i(120);   // 2^-e_cur
     float sv_lim = -1.f;     // a step above this moves e_cur
-    const int lo_min = I.lo_min, lo_max = I.lo_max, hi_min = I.hi_min;
+    uint32_t n_done = 0;     // blocks this warp has added to O
+    const int lo_min = I.lo_min, lo_max = I.lo_max, hi_min = I.hi_min, hi_max = I.hi_max;
 
     for (int kb = kw / SUB; kb < n_blk; kb += KW / SUB) {
       const uint32_t cb = cnt + kb;
@@ -530,7 +535,7 @@ __global__ void __launch_bounds__(I4Cfg<NT>::THREADS, I4Cfg<NT>::CTAS) decode_i4
       uint8_t* vs = ks + SM::BLK;
       const bool is_new = kb >= n_cached;
       const int kbase = is_new ? L : ia + kb * 64;
-      const int kend = is_new ? L + p.n_qt : ib;  // no key at or past this
+      const int kend = min(is_new ? L + p.n_qt : ib, hi_max);  // no key any row sees at or past this
       const bool edge = kbase + 64 > min(kend, hi_min) || kbase < lo_max;
 #pragma unroll 1
       for (int k0 = (kw % SUB) * 16 * GW; k0 < (kw % SUB + 1) * 16 * GW; k0 += 16 * KU) {
@@ -662,6 +667,7 @@ __global__ void __launch_bounds__(I4Cfg<NT>::THREADS, I4Cfg<NT>::CTAS) decode_i4
               m[nt][c] = mn;
               l[nt][c] *= al;
               bs[nt][c] *= al;
+              l_sh[nt][c] *= al;
               const float f = al * osc;
 #pragma unroll
               for (int i = 0; i < MT; ++i) {
@@ -727,6 +733,32 @@ __global__ void __launch_bounds__(I4Cfg<NT>::THREADS, I4Cfg<NT>::CTAS) decode_i4
                 const int i = 4 * h + 2 * q + y;  // dims 2i (rows 0-7) and 2i + 1 (rows 8-15) of this lane's
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) mma_f16(o[i][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+              }
+            }
+        }
+      }
+      // Every 4 blocks, move the codes' mean out of O: sum P c is 7.5 step sum p plus a small rest, and the
+      // tensor core's accumulation truncates, so over thousands of keys the rest (all that is left after
+      // sum p lo is added) lost 0.2% of its size to the large common part. Any S may be taken from O as long
+      // as the same S is added to sum p lo; S = 7.5 (some key's step) (sum p since the last time).
+      if ((++n_done & 3u) == 0) {
+        const float sbar = __shfl_sync(0xffffffffu, __uint_as_float(*i4_pair<D>(vs, 64, 0) << 16), 0);
+        if (!is_new && sbar > 0.f) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float d = l[nt][c] - l_sh[nt][c];
+              l_sh[nt][c] = l[nt][c];
+#pragma unroll
+              for (int x = 4; x < 32; x <<= 1) d += __shfl_xor_sync(0xffffffffu, d, x);
+              const float S = 7.5f * sbar * d;
+              bs[nt][c] += 0.125f * S;  // the 8 lanes of a row are summed at the end
+              const float se = S * fe * 5.9604645e-8f, so = S * fe * 9.5367432e-7f;  // 2^-24, 2^-20
+#pragma unroll
+              for (int i = 0; i < MT; ++i) {
+                o[i][nt][c] -= se;
+                o[i][nt][2 + c] -= so;
               }
             }
         }

@@ -305,7 +305,7 @@ int kv_pool_set_scales(hswa_pool* pool, int layer, const float* k_scale, const f
     return HSWA_ERR_INVALID_ARG;
   }
   if (!pool->fp8) {
-    set_error("kv_pool_set_scales: the pool stores bf16 entries; scales apply to FP8 pools");
+    set_error("kv_pool_set_scales: the pool stores bf16 or 4-bit entries; scales apply to FP8 pools");
     return HSWA_ERR_INVALID_ARG;
   }
   const hswa_pool_desc& D = pool->desc;
@@ -519,8 +519,8 @@ static int check_mod(const hswa_score_mod* mod, const char* who) {
     set_error("%s: null score modifications", who);
     return HSWA_ERR_INVALID_ARG;
   }
-  if (!(mod->softcap >= 0.0f) || !isfinite(mod->softcap)) {
-    set_error("%s: softcap must be 0 or finite and > 0", who);
+  if (mod->softcap != 0.0f && !(mod->softcap >= 1e-6f && mod->softcap <= 1e6f)) {
+    set_error("%s: softcap must be 0 or in 1e-6 .. 1e6", who);
     return HSWA_ERR_INVALID_ARG;
   }
   return HSWA_OK;
@@ -696,13 +696,7 @@ int hybrid_decode_workspace_size(const hswa_pool* pool, int n_seqs, int n_q_per_
   const hswa_pool_desc& D = pool->desc;
   // sized for a full layer, the larger of the two layer kinds; 4-bit pools and modified scores may cut
   // the keys into shorter splits, and so need more
-  *bytes = decode_workspace_bytes(n_seqs, n_q_per_seq, n_q_heads, D.n_kv_heads, D.head_dim, 0, max_ctx_len, false);
-  const size_t ext =
-      decode_workspace_bytes(n_seqs, n_q_per_seq, n_q_heads, D.n_kv_heads, D.head_dim, 0, max_ctx_len, true);
-  const size_t ext_ring = decode_workspace_bytes(n_seqs, n_q_per_seq, n_q_heads, D.n_kv_heads, D.head_dim, D.window,
-                                                 max_ctx_len, true);
-  if (ext > *bytes) *bytes = ext;
-  if (D.n_swa_layers > 0 && ext_ring > *bytes) *bytes = ext_ring;
+  *bytes = decode_workspace_bound(n_seqs, n_q_per_seq, n_q_heads, D.n_kv_heads, D.head_dim, max_ctx_len);
   return HSWA_OK;
 }
 

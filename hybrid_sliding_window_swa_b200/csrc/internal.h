@@ -164,6 +164,8 @@ struct DecodeLaunch {
   size_t ws_bytes;
 };
 
+// What the size query returns: enough for any call with at most these sequences and this context length.
+size_t decode_workspace_bound(int n_seqs, int n_qt, int Hq, int Hkv, int d, int64_t max_ctx_len);
 size_t decode_workspace_bytes(int n_seqs, int n_qt, int Hq, int Hkv, int d, int window, int64_t max_ctx_len, bool ext);
 // Dynamic shared memory of the split merge for these arguments (0 when no sequence can have two splits).
 size_t decode_merge_smem_bytes(int n_seqs, int n_qt, int Hq, int Hkv, int window, int64_t max_ctx_len);

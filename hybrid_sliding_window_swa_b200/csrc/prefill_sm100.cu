@@ -422,16 +422,20 @@ __device__ __forceinline__ void ring_tile_cpasync(const Params& p, const Geo& G,
   if (!seq_ok && lane == 0) record_error(p.err, HSWA_ERR_DEVICE_BOUNDS);
   const int64_t row_base = seq_ok ? (((int64_t)seq * p.n_swa + p.ring_layer) * p.Hkv + G.g) * p.window : 0;
   int held_lo = (G.P - p.window > 0) ? G.P - p.window : 0;
-  if constexpr (MOD) held_lo = max(held_lo, G.kmin);  // rows no query of the unit sees are not read
+  int held_hi = G.P;
+  if constexpr (MOD) {  // rows no query of the unit sees are not read
+    held_lo = max(held_lo, G.kmin);
+    held_hi = min(held_hi, G.kmax + 1);
+  }
   if constexpr (I4) {
     const int64_t blk = seq_ok ? (((int64_t)seq * p.n_swa + p.ring_layer) * p.Hkv + G.g) * p.blk_bytes : 0;
-    ring_rows_i4<D>((ring == p.ring_v ? p.ring_v8 : p.ring_k8) + blk, seq_ok, held_lo, G.P, p.window, dst, kb, lane);
+    ring_rows_i4<D>((ring == p.ring_v ? p.ring_v8 : p.ring_k8) + blk, seq_ok, held_lo, held_hi, p.window, dst, kb, lane);
   } else if (p.fp8) {
     const bool is_v = ring == p.ring_v;
-    ring_rows_fp8<D>((is_v ? p.ring_v8 : p.ring_k8) + row_base * D, seq_ok, held_lo, G.P, p.window,
+    ring_rows_fp8<D>((is_v ? p.ring_v8 : p.ring_k8) + row_base * D, seq_ok, held_lo, held_hi, p.window,
                      is_v ? p.v_scale[G.g] : p.k_scale[G.g], dst, kb, lane);
   } else {
-    ring_rows_cpasync<D>(ring + row_base * D, seq_ok, held_lo, G.P, p.window, dst, kb, lane);
+    ring_rows_cpasync<D>(ring + row_base * D, seq_ok, held_lo, held_hi, p.window, dst, kb, lane);
   }
 }
 
@@ -742,7 +746,7 @@ __device__ void producer(const Params& p, uint8_t* smem, Bars* bars, const CUten
               if (lane == 0) mbar_arrive(full);
             }
           }
-        } else if (ring_fast && (!MOD || kmin <= kb)) {
+        } else if (ring_fast && (!MOD || (kmin <= kb && kmax >= kb + BN - 1))) {
           if (lane == 0) {
             mbar_arrive_expect_tx(full, L::TILE);
             const CUtensorMap* tm = kv ? tm_rv : tm_rk;

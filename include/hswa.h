@@ -169,7 +169,8 @@ typedef struct hswa_rope_desc {
  *  pos       device int64[n_axes][n_tokens]
  *  q, q_out  [n_tokens][n_q_heads][head_dim] bf16;  k, k_out [n_tokens][n_kv_heads][head_dim] bf16.
  * q_out may be q and k_out may be k (in place); other overlaps are not allowed. n_q_heads or
- * n_kv_heads may be 0 (its pointers are then not used). Runs on the current device. */
+ * n_kv_heads may be 0 (its pointers are then not used). Runs on the current device, which must hold the
+ * tensors. */
 HSWA_API int rope_fwd(const hswa_rope_desc* rope, int head_dim, int64_t n_tokens, const int64_t* pos,
                       const hswa_bf16* q, hswa_bf16* q_out, int n_q_heads, const hswa_bf16* k, hswa_bf16* k_out,
                       int n_kv_heads, void* stream);
@@ -227,7 +228,8 @@ HSWA_API int full_prefill_fwd(hswa_pool* pool, int layer, const hswa_bf16* q, hs
                      int n_q, const int64_t* start_pos, const int32_t* page_table, int pt_stride,
                      int n_q_heads, void* stream);
 
-/* Bytes of device workspace hybrid_decode_fwd needs for these arguments. */
+/* Bytes of device workspace hybrid_decode_fwd needs for these arguments, and for any call with fewer
+ * sequences, fewer new tokens or shorter contexts. */
 HSWA_API int hybrid_decode_workspace_size(const hswa_pool* pool, int n_seqs, int n_q_per_seq,
                                  int n_q_heads, int64_t max_ctx_len, size_t* bytes);
 
@@ -271,7 +273,7 @@ HSWA_API int hybrid_decode_fwd(hswa_pool* pool, int layer, const hswa_bf16* q, c
  * the smallest and the largest position the queries of a sequence see; outside it they may hold anything,
  * and pages of such positions are not read. */
 typedef struct hswa_score_mod {
-  float softcap;             /* 0: none; else finite and > 0 */
+  float softcap;             /* 0: none; else 1e-6 .. 1e6 */
   const float* dist_slope;   /* device float32[n_q_heads], finite; NULL: none */
   const int64_t* key_begin;  /* device int64[B][n_q], any values; NULL: 0 */
   const int64_t* key_end;    /* device int64[B][n_q], any values; NULL: i + 1 */

@@ -157,6 +157,17 @@ def test_decode_over_ring(W, n_qt, hq, hkv, d):
         ref.check(o[b], r, f"W={W} seq {b} L={lens[b]}")
 
 
+def test_decode_of_more_sequences_than_a_warp():
+    # past 32 sequences the work list comes from its own kernel
+    lens = [(37 * i * i + 5 * i) % 700 for i in range(41)] + [9000]
+    o, refs = decode_case(17, lens, 2, 4, 2, 64, 0)
+    for b, r in enumerate(refs):
+        ref.check(o[b], r, f"seq {b} L={lens[b]}")
+    o, refs = decode_case(18, lens[:40], 1, 4, 2, 64, 128)
+    for b, r in enumerate(refs):
+        ref.check(o[b], r, f"ring seq {b} L={lens[b]}")
+
+
 @pytest.mark.parametrize("spread,q_scale", [(1e-4, 3e3), (300.0, 3e-3), (1e4, 1e-4), (1e-20, 1e20)])
 def test_decode_range_of_values(spread, q_scale):
     # scores of ordinary size from entries far from 1: the f16 operands are scaled per row and per step
@@ -220,3 +231,24 @@ def test_bad_page_and_ring_row_are_reported():
     hs.kv_pool_append(pool, 1, q, q, torch.tensor([64], device="cuda"), page_table=pt)
     assert hs.hswa_pool_check_error(pool) == hs.HSWA_ERR_DEVICE_BOUNDS
     assert (pool.data == 0).all()
+
+
+def test_a_workspace_serves_every_smaller_call():
+    hq, hkv, d, big = 4, 1, 64, 8192
+    pool = make_pool(hkv, d, 0, 1, 1, 1, 130)
+    pt = torch.arange(130, dtype=torch.int32).view(1, 130).cuda()
+    k, v = rows(1, big, hkv, d)[None].cuda(), rows(2, big, hkv, d)[None].cuda()
+    hs.kv_pool_append(pool, 0, k, v, torch.tensor([0]).cuda(), page_table=pt)
+    ws = torch.empty(hs.hybrid_decode_workspace_size(pool, 40, 2, hq, big), dtype=torch.uint8, device="cuda")
+    want = {}
+    for n in (1, 2, 5, 8, 31, 33, 40):
+        for L in (1, 700, 5000, big):
+            assert hs.hybrid_decode_workspace_size(pool, n, 2, hq, L) <= ws.numel()
+            q, kn, vn = (rows(s, 2, h, d)[None].expand(n, 2, h, d).contiguous().cuda() for s, h in ((3, hq), (4, hkv), (5, hkv)))
+            ctx = torch.full((n,), L, dtype=torch.int64).cuda()
+            o = hs.hybrid_decode_fwd(pool, 0, q, kn, vn, ctx, L, ws, page_table=pt.expand(n, 130).contiguous())
+            want.setdefault(L, o[0].float())
+            # the same sequence however the batch cuts it into splits: one rounding of the output apart,
+            # and the f16 weights' (2^-11 of the weighted codes)
+            assert (o.float() - want[L]).abs().max() <= 2.0 ** -7 * want[L].abs().max() + 2.0 ** -9 * 8
+    assert hs.hswa_pool_check_error(pool) == 0

@@ -237,6 +237,28 @@ def test_decode(fmt, cap, bias, mask, lens, n_qt, hq, hkv, d, W):
     decode_case(fmt, lens, n_qt, hq, hkv, d, W, cap, bias, mask)
 
 
+@pytest.mark.parametrize("fmt", [BF, F8, I4])
+def test_padded_new_tokens_may_hold_anything(fmt):
+    # rows 2 and 3 of a step are padding: they see nothing, nothing sees them, their k and v are NaN
+    hq, hkv, d, L = 4, 2, 64, 100
+    pool = make_pool(fmt, hkv, d, 0, 1, 64, 1, 3)
+    pt = torch.tensor([[2, 0]], dtype=torch.int32).cuda()
+    k, v, q = randn(1, L + 2, hkv, d), randn(2, L + 2, hkv, d), randn(3, 4, hq, d)
+    hs.kv_pool_append(pool, 0, k[None, :L].cuda(), v[None, :L].cuda(), torch.tensor([0]).cuda(), page_table=pt)
+    nan = torch.full((2, hkv, d), float("nan"), dtype=torch.bfloat16)
+    end = torch.tensor([[L + 1, L + 2, 0, 0]])
+    ws = torch.empty(hs.hybrid_decode_workspace_size(pool, 1, 4, hq, L), dtype=torch.uint8, device="cuda")
+    o = hs.hybrid_decode_mod_fwd(pool, 0, q[None].cuda(), torch.cat([k[L:], nan])[None].cuda(),
+                                 torch.cat([v[L:], nan])[None].cuda(), torch.tensor([L]).cuda(), L,
+                                 hs.ScoreMod(key_end=end.cuda()), ws, page_table=pt)
+    assert hs.hswa_pool_check_error(pool) == 0
+    assert (o[0, 2:] == 0).all()
+    lo, hi = ref.ranges(2, L, L + 2)
+    hv = held(fmt, v, False)
+    ref.check(o[0, :2], ref.attention(q[:2], held(fmt, k, False), hv, lo, hi, weight_eps=ref.F16 if fmt == I4 else ref.BF16,
+                                      v_range=hv.amax(-1) - hv.amin(-1) if fmt == I4 else None), "real rows")
+
+
 def test_decode_range_far_into_a_long_context():
     # only the last document of a long context is seen: the splits start at its page
     decode_case(I4, [30000, 9000], 2, 4, 1, 64, mask="docs")
