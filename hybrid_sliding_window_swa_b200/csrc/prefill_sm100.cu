@@ -1051,6 +1051,7 @@ __global__ void __launch_bounds__(I4 ? NTHREADS_I4 : NTHREADS, 1)
 int launch_prefill(const PrefillLaunch& Lc, cudaStream_t stream) {
   // narrow windows: every query tile's band fits in two key tiles, which stay resident while
   // all query heads of a KV head pass through them
+  // (modified scores stay here for every window)
   if (!Lc.mod && Lc.window >= 1 && Lc.window <= BN + 1) return launch_prefill_narrow(Lc, stream);
   const hswa_pool* pool = Lc.pool;
   const hswa_pool_desc& D = pool->desc;

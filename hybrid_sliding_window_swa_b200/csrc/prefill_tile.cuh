@@ -90,21 +90,50 @@ inline void fill_score_params(const hswa_score_mod& m, double scale, ScoreParams
   }
 }
 
-// The 128 raw scores of a row -> z log2(e), z = cap tanh(s / cap) - slope |i - j|. c_q: the query's own
-// column (its position minus the tile's), so column k is |c_q - k| away.
+// Largest magnitude of a row's raw scores (NaN ignored).
+template <int N>
+__device__ __forceinline__ float abs_max(const uint32_t (&v)[N]) {
+  float m0 = 0.f, m1 = 0.f, m2 = 0.f, m3 = 0.f;
+#pragma unroll
+  for (int k = 0; k < N; k += 8) {
+    m0 = fmax3(m0, fabsf(__uint_as_float(v[k])), fabsf(__uint_as_float(v[k + 1])));
+    m1 = fmax3(m1, fabsf(__uint_as_float(v[k + 2])), fabsf(__uint_as_float(v[k + 3])));
+    m2 = fmax3(m2, fabsf(__uint_as_float(v[k + 4])), fabsf(__uint_as_float(v[k + 5])));
+    m3 = fmax3(m3, fabsf(__uint_as_float(v[k + 6])), fabsf(__uint_as_float(v[k + 7])));
+  }
+  return fmaxf(fmax3(m0, m1, m2), m3);
+}
+
+// The N raw scores of a row -> z log2(e), z = cap tanh(s / cap) - slope |i - j|. c_q: the query's own
+// column (its position minus that of column 0), so column k is |c_q - k| away.
 // The cap costs what tanh costs: through exponential and reciprocal it is two more MUFU operations per
 // score, on the unit that the softmax itself loads most. While every score of the warp stays within the
-// cap (|s| <= cap), the degree-11 polynomial on the FMA pipe replaces them: 7 packed multiply-adds per pair.
+// cap (|s| <= cap), the degree-11 polynomial on the FMA pipe replaces them: 7 packed multiply-adds per pair;
+// within 0.35 cap a degree-5 one does, 4 per pair.
 // Bias: on a tile wholly before the warp's queries |c_q - k| = c_q - k, two packed operations per pair.
-__device__ __forceinline__ void modify_scores(uint32_t (&v)[128], const ScoreParams& sp, float sl2, float slope2,
-                                              float c_q, float abs_max) {
+// am: abs_max(v), used with a cap.
+template <int N>
+__device__ __forceinline__ void modify_scores(uint32_t (&v)[N], const ScoreParams& sp, float sl2, float slope2,
+                                              float c_q, float am) {
   if (sp.softcap > 0.f) {
-    if (__all_sync(0xffffffffu, abs_max <= sp.poly_max)) {
+    if (__all_sync(0xffffffffu, am <= sp.near_max)) {
+      const uint64_t n0 = f2_pack(sp.near[0], sp.near[0]), n1 = f2_pack(sp.near[1], sp.near[1]),
+                     n2 = f2_pack(sp.near[2], sp.near[2]);
+#pragma unroll
+      for (int k = 0; k < N; k += 2) {
+        const uint64_t x = f2_pack(__uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+        const uint64_t t = f2_mul(x, x);
+        float a, b;
+        f2_unpack(f2_mul(x, f2_fma(f2_fma(n2, t, n1), t, n0)), a, b);
+        v[k] = __float_as_uint(a);
+        v[k + 1] = __float_as_uint(b);
+      }
+    } else if (__all_sync(0xffffffffu, am <= sp.poly_max)) {
       uint64_t c[6];
 #pragma unroll
       for (int i = 0; i < 6; ++i) c[i] = f2_pack(sp.poly[i], sp.poly[i]);
 #pragma unroll
-      for (int k = 0; k < 128; k += 2) {
+      for (int k = 0; k < N; k += 2) {
         const uint64_t x = f2_pack(__uint_as_float(v[k]), __uint_as_float(v[k + 1]));
         const uint64_t t = f2_mul(x, x);
         uint64_t y = f2_fma(c[5], t, c[4]);
@@ -120,18 +149,18 @@ __device__ __forceinline__ void modify_scores(uint32_t (&v)[128], const ScorePar
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < 128; ++k)
+      for (int k = 0; k < N; ++k)
         v[k] = __float_as_uint(capped_log2(__uint_as_float(v[k]), sp.cap_in, sp.cap_log2));
     }
     sl2 = 1.f;
   }
   if (sp.slope) {
-    if (__all_sync(0xffffffffu, c_q >= 127.f)) {
+    if (__all_sync(0xffffffffu, c_q >= (float)(N - 1))) {
       // x sl2 + slope2 (k - c_q), k - c_q exact
       const uint64_t s2 = f2_pack(sl2, sl2), b2 = f2_pack(slope2, slope2), two = f2_pack(2.f, 2.f);
       uint64_t d = f2_pack(-c_q, 1.f - c_q);
 #pragma unroll
-      for (int k = 0; k < 128; k += 2) {
+      for (int k = 0; k < N; k += 2) {
         float a, b;
         f2_unpack(f2_fma(f2_pack(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), s2, f2_mul(d, b2)), a, b);
         v[k] = __float_as_uint(a);
@@ -140,7 +169,7 @@ __device__ __forceinline__ void modify_scores(uint32_t (&v)[128], const ScorePar
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < 128; ++k)
+      for (int k = 0; k < N; ++k)
         v[k] = __float_as_uint(fmaf(-slope2, fabsf(c_q - (float)k), __uint_as_float(v[k]) * sl2));
     }
   }
@@ -191,15 +220,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t trow, uint32_t s_col, uint
     if constexpr (MOD) {
       float am = 0.f;
       if (sp->softcap > 0.f) {
-        float m0 = 0.f, m1 = 0.f, m2 = 0.f, m3 = 0.f;
-#pragma unroll
-        for (int k = 0; k < 128; k += 8) {
-          m0 = fmax3(m0, fabsf(__uint_as_float(v[k])), fabsf(__uint_as_float(v[k + 1])));
-          m1 = fmax3(m1, fabsf(__uint_as_float(v[k + 2])), fabsf(__uint_as_float(v[k + 3])));
-          m2 = fmax3(m2, fabsf(__uint_as_float(v[k + 4])), fabsf(__uint_as_float(v[k + 5])));
-          m3 = fmax3(m3, fabsf(__uint_as_float(v[k + 6])), fabsf(__uint_as_float(v[k + 7])));
-        }
-        am = fmaxf(fmax3(m0, m1, m2), m3);
+        am = abs_max(v);
         near = __all_sync(0xffffffffu, am <= sp->near_max) && !sp->slope;
       }
       if (!near) {

@@ -169,7 +169,8 @@ def test_full_prefill_reads_only_what_is_seen(fmt, mask):
 @pytest.mark.parametrize("fmt", [BF, F8, I4])
 @pytest.mark.parametrize("W,starts", [(1, [9]), (40, [0, 100]), (128, [128, 256]), (129, [33, 0]), (300, [700, 40]),
                                       (512, [512, 1024])])
-@pytest.mark.parametrize("cap,bias,mask", [(10.0, False, "none"), (0.0, True, "prefix"), (25.0, True, "docs")])
+@pytest.mark.parametrize("cap,bias,mask", [(10.0, False, "none"), (0.0, True, "prefix"), (25.0, True, "docs"),
+                                           (0.0, True, "none"), (3.0, True, "none")])
 def test_swa_prefill(fmt, W, starts, cap, bias, mask):
     prefill_case("swa", fmt, starts, 270, 4, 2, 128, W=W, cap=cap, bias=bias, mask=mask)
 
