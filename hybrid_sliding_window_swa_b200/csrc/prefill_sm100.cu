@@ -855,8 +855,11 @@ __device__ void mma_issuer(const Params& p, uint8_t* smem, Bars* bars, uint32_t 
     umma_commit(&bars->q_empty);
     // drain the last tile's P V products and release its V stage
     bool v_ready = false;
-    for (int q = 0; q < NQT; ++q)
+    for (int q = 0; q < NQT; ++q) {
       if (pend[q] && !drain_q(q, v_ready)) return;
+      // modified scores: a slot's output is handed over before the other slot's last product is waited for
+      if (MOD && G.act[q] && G.jhi[q] >= G.jlo[q]) umma_commit(&bars->o_full[q]);
+    }
     if (have_prev) {
       if (!v_ready) {
         if (!mbar_wait(&bars->v_full[prev_s], prev_ph, p.err)) return;
@@ -865,7 +868,7 @@ __device__ void mma_issuer(const Params& p, uint8_t* smem, Bars* bars, uint32_t 
       umma_commit(&bars->v_empty[prev_s]);
     }
     for (int q = 0; q < NQT; ++q)
-      if (G.act[q] && (!MOD || G.jhi[q] >= G.jlo[q])) umma_commit(&bars->o_full[q]);
+      if (!MOD && G.act[q]) umma_commit(&bars->o_full[q]);
   }
 }
 
