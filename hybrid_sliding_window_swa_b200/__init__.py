@@ -137,6 +137,8 @@ def _check(rc: int):
 def _ptr(t: torch.Tensor | None, dtype=None, name: str = "tensor"):
     if t is None:
         return None
+    if t.dtype is dtype and t.is_cuda and t.is_contiguous():  # the usual call, a few per microsecond
+        return t.data_ptr()
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
@@ -148,13 +150,14 @@ def _ptr(t: torch.Tensor | None, dtype=None, name: str = "tensor"):
 
 # The current stream's handle without building a Stream object (3.5 us a call, more than a small kernel).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _stream(stream=None):
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_current_device())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -348,7 +351,7 @@ def rope_fwd(rope: RopeDesc, q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor
     d = qs[-1]
     if qs[:-2] != ks[:-2] or d != ks[-1]:
         raise ValueError("q and k must have the same tokens and head_dim")
-    if q.device.index != torch.cuda.current_device() or k.device != q.device or pos.device != q.device:
+    if not q.get_device() == k.get_device() == pos.get_device() == (_current_device() if q.is_cuda else -2):
         raise ValueError("q, k and pos must be on the current CUDA device")
     n = math.prod(qs[:-2])
     if pos.shape[0] != rope.n_axes or pos.numel() != rope.n_axes * n:

@@ -1292,6 +1292,9 @@ int ext_split(int n_seqs, int Hkv, int window, int64_t max_ctx_len) {
     const int64_t least = split < 2048 ? split : 2048;
     split = fine > least ? fine : least;
   }
+  // a context of a few pages is one split: its 4 warps walk 8 blocks in less than a merge and its launch
+  // take (400 keys: 10.2 us a call against 12.3 with splits of 256; 613 keys: 12.3 against 11.7)
+  if (cached <= 512) return 512;
   split = (split + 63) / 64 * 64;
   return (int)(split < 256 ? 256 : (split > SPLIT ? SPLIT : split));
 }

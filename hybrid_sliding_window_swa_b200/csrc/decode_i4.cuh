@@ -117,7 +117,8 @@ struct I4Smem {
   static constexpr int AREA_STRIDE = D + 4;  // floats
   static constexpr int Q_OFF = 0;
   static constexpr int AREA_OFF = Q_OFF + 2 * Q_BYTES;
-  static constexpr int ML_OFF = AREA_OFF + 2 * ROWS * AREA_STRIDE * 4;
+  static constexpr int AREAS = RG == 2 ? CFG::W / 2 : CFG::W;  // one per warp of a row group
+  static constexpr int ML_OFF = AREA_OFF + AREAS * ROWS * AREA_STRIDE * 4;
   // m, l, sum p lo per (warp, row), then per row
   static constexpr int ROW_OFF = ML_OFF + (3 * CFG::W * ROWS + 3 * ROWS) * 4;  // per row: token, output offset
   static constexpr int ITEM_OFF = ROW_OFF + 2 * ROWS * 4;
@@ -156,6 +157,16 @@ __global__ void __launch_bounds__(I4Cfg<NT>::THREADS, I4Cfg<NT>::CTAS) decode_i4
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   WsHeader* hdr = reinterpret_cast<WsHeader*>(p.ws);
 
+  // what the producer needs first is read before the barriers are set up
+  const int err0 = p.small && tid == 0 ? read_error(p.err) : 0;
+  int sp_L = 0, sp_body = 0, sp_excl = 0, sp_total = 0;
+  if (p.small && warp == I4_WARPS) {
+    const SmallPlan sp(p);
+    sp_L = sp.L;
+    sp_body = sp.body;
+    sp_excl = sp.excl;
+    sp_total = sp.total;
+  }
   int* row_tok = reinterpret_cast<int*>(smem + SM::ROW_OFF);  // new token of a query row
   int* row_out = row_tok + ROWS;  // its place in the output, from (sequence, first token, first head of g)
   for (int r = tid; r < ROWS; r += CFG::THREADS) {
@@ -177,21 +188,17 @@ __global__ void __launch_bounds__(I4Cfg<NT>::THREADS, I4Cfg<NT>::CTAS) decode_i4
   }
   grid_go();    // the merge may take its place; it waits for this grid's end before it reads
   grid_wait();  // the work list
-  if (tid == 0) *go = read_error(p.err) == 0;
+  if (tid == 0) *go = (p.small ? err0 : read_error(p.err)) == 0;
   __syncthreads();
   if (!*go) return;  // a pending device error: skip the work
 
   if (warp == I4_WARPS) {
     // ------------------------------------------------------------ producer
     const PlanView pv(p.ws, p.n_seqs);
-    int sp_L = 0, sp_body = 0, sp_excl = 0, total, body_total;
+    int total, body_total;
     if (p.small) {
-      const SmallPlan sp(p);
-      sp_L = sp.L;
-      sp_body = sp.body;
-      sp_excl = sp.excl;
-      body_total = sp.total;
-      total = (sp.total + p.n_seqs) * p.Hkv;
+      body_total = sp_total;
+      total = (sp_total + p.n_seqs) * p.Hkv;
     } else {
       body_total = hdr->body_total;
       total = hdr->total_items;
@@ -779,7 +786,7 @@ __global__ void __launch_bounds__(I4Cfg<NT>::THREADS, I4Cfg<NT>::CTAS) decode_i4
           l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], x);
           bs[nt][c] += __shfl_xor_sync(0xffffffffu, bs[nt][c], x);
         }
-    if (!cons_sync()) return;  // the previous item's output has been read
+    if (it > 0 && !cons_sync()) return;  // the previous item's output has been read
     if (lane == 0) mbar_arrive(&item_empty[slot]);
     if (g8 == 0) {
 #pragma unroll
@@ -806,7 +813,7 @@ __global__ void __launch_bounds__(I4Cfg<NT>::THREADS, I4Cfg<NT>::CTAS) decode_i4
         bb += b_w[w * ROWS + tid] * f;
       }
       m_all[tid] = M;
-      l_all[tid] = ls;
+      l_all[tid] = nsp == 1 ? (ls == 0.f ? 0.f : 1.f / ls) : ls;  // (a row that sees nothing: 0)
       b_all[tid] = bb;
     }
     {
@@ -822,39 +829,34 @@ __global__ void __launch_bounds__(I4Cfg<NT>::THREADS, I4Cfg<NT>::CTAS) decode_i4
           f[nt][c] = M == -INFINITY ? 0.f : ex2_approx(m[nt][c] - M) * pow2i(e_cur);
         }
       // O^T accumulators: dims 2i hold 2^-24, dims 2i + 1 hold 2^-20 of the sum
-      auto put = [&](bool add) {
+      {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const int r = row0 + nt * 8 + 2 * t4 + c;
-            float* dst = area + ((kw & 1) * ROWS + r) * SM::AREA_STRIDE + g8 * (D / 8);
+            float* dst = area + (kw * ROWS + r) * SM::AREA_STRIDE + g8 * (D / 8);
 #pragma unroll
             for (int i = 0; i < MT; i += 2) {
-              float4 y = make_float4(o[i][nt][c] * f[nt][c] * 16777216.f, o[i][nt][2 + c] * f[nt][c] * 1048576.f,
+              const float4 y = make_float4(o[i][nt][c] * f[nt][c] * 16777216.f, o[i][nt][2 + c] * f[nt][c] * 1048576.f,
                                      o[i + 1][nt][c] * f[nt][c] * 16777216.f,
                                      o[i + 1][nt][2 + c] * f[nt][c] * 1048576.f);
-              float4* d4 = reinterpret_cast<float4*>(dst + 2 * i);
-              if (add) {
-                const float4 z = *d4;
-                y.x += z.x; y.y += z.y; y.z += z.z; y.w += z.w;
-              }
-              *d4 = y;
+              *reinterpret_cast<float4*>(dst + 2 * i) = y;
             }
           }
-      };
-#pragma unroll 1
-      for (int rnd = 0; rnd < (KW + 1) / 2; ++rnd) {  // two warps of a row group at a time, one per area
-        if ((kw >> 1) == rnd) put(rnd > 0);
-        if (!cons_sync()) return;
       }
+      if (!cons_sync()) return;
     }
     // ---- output: bf16 rows when the sequence has one split, else this item's partial
     auto merged4 = [&](int r, int c) -> float4 {
-      const float4 x = *reinterpret_cast<const float4*>(area + r * SM::AREA_STRIDE + c);
-      const float4 y = *reinterpret_cast<const float4*>(area + (ROWS + r) * SM::AREA_STRIDE + c);
       const float bb = b_all[r];
-      return make_float4(x.x + y.x + bb, x.y + y.y + bb, x.z + y.z + bb, x.w + y.w + bb);
+      float4 x = make_float4(bb, bb, bb, bb);
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        const float4 y = *reinterpret_cast<const float4*>(area + (w * ROWS + r) * SM::AREA_STRIDE + c);
+        x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+      }
+      return x;
     };
     float* part = reinterpret_cast<float*>(p.ws + p.part_off + (size_t)item * p.part_bytes);
     uint16_t* out = p.o + ((int64_t)s * p.n_qt * p.Hq + hg * p.G) * D;
@@ -863,10 +865,8 @@ __global__ void __launch_bounds__(I4Cfg<NT>::THREADS, I4Cfg<NT>::CTAS) decode_i4
       const int r = idx / (D / 4), c = (idx % (D / 4)) * 4;
       float4 x = merged4(r, c);
       if (nsp == 1) {
-        const float ls = l_all[r];
-        const float inv = 1.f / ls;
-        if (ls == 0.f) x = make_float4(0.f, 0.f, 0.f, 0.f);  // a row that sees nothing
-        else x = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+        const float inv = l_all[r];
+        x = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
         uint2 pk;
         pk.x = pack_bf16x2(x.x, x.y);
         pk.y = pack_bf16x2(x.z, x.w);
