@@ -1329,16 +1329,16 @@ template <int D, int NT, int RG, bool MOD>
 int launch_i4(DecParams& p, int n_items_max, int sms, int device, int64_t nsp_max, cudaStream_t stream) {
   using SM = I4Smem<D, NT, RG>;
   HSWA_SET_SMEM((decode_i4_kernel<D, NT, RG, MOD>), SM::BYTES, device);
-  int grid = sms * I4Cfg<NT>::CTAS;
+  int grid = sms * I4_CTAS;
   if (grid > n_items_max) grid = n_items_max;
   if (grid < 1) grid = 1;
   p.small = p.n_seqs <= 32 ? 1 : 0;
   cudaError_t e = cudaSuccess;
   if (p.small) {
-    decode_i4_kernel<D, NT, RG, MOD><<<grid, I4Cfg<NT>::THREADS, SM::BYTES, stream>>>(p);
+    decode_i4_kernel<D, NT, RG, MOD><<<grid, I4_THREADS, SM::BYTES, stream>>>(p);
   } else {
     plan_kernel<true><<<1, 1024, 0, stream>>>(p);
-    e = launch_dependent(decode_i4_kernel<D, NT, RG, MOD>, grid, I4Cfg<NT>::THREADS, SM::BYTES, stream, p);
+    e = launch_dependent(decode_i4_kernel<D, NT, RG, MOD>, grid, I4_THREADS, SM::BYTES, stream, p);
   }
   if (e == cudaSuccess && nsp_max > 1) e = launch_merge_rows<D>(p, nsp_max, stream);
   if (e == cudaSuccess) e = cudaGetLastError();

@@ -27,23 +27,18 @@
 // brings the largest so far to 2^6 .. 2^7; a larger one raises it and rescales O. P keeps its 11 bits
 // down to 2^-20 of the largest p * step.
 //
-// What bounds it. 2 (d / 2 + 4) bytes per key and KV head against about 100 integer, 16 ldmatrix-free
-// shared loads and 16 MMAs per 16 keys and 8 rows. Bytes for up to 8 rows, the MMA rate for 32.
+// What bounds it. 2 (d / 2 + 4) bytes per key and KV head. Up to 8 rows the reads do: 5.2 TB/s while the items
+// of a 256K-token sequence run (72 us the call; its 285 MB take 43 us). With 32 rows the instruction dispatch
+// does: integer 40%, MMA 40%, fp32 12% of the cycles (ncu), which add up; neither more warps nor more
+// registers nor issuing the next block's S among the V products moved it.
 //
 // Structure: 4 consumer warps and a producer warp per CTA, two CTAs per SM, taking items from the work
 // list. A block is one 64-key page: (codes, pairs) of K and of V are contiguous, one bulk copy each
 // (cp.async for ring rows, whose runs may start anywhere), several blocks ahead, across items. The
 // producer also hands over the item's geometry and its Q rows. The warps take blocks in turn (for more
-// than 16 rows in pairs, half the rows each), 32 or 64 keys at a time so that enough independent MMAs are
+// than 16 rows in pairs, half the rows each), 32 keys at a time so that enough independent MMAs are
 // in flight, and merge their softmax states at the end of the item.
 // Waits are bounded; a failing wait makes its warp return and the others run out theirs.
-
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
 
 __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
@@ -79,22 +74,13 @@ __device__ __forceinline__ void mma_f16_zero(float (&c)[4], uint32_t a0, uint32_
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 
-#ifndef HSWA_I4_CFG1
-#define HSWA_I4_CFG1 0x4221
-#endif
-#ifndef HSWA_I4_CFG2
-#define HSWA_I4_CFG2 0x4221
-#endif
-template <int X>
-struct I4CfgT {
-  static constexpr int W = X >> 12;            // consumer warps per CTA
-  static constexpr int CTAS = (X >> 8) & 15;   // CTAs per SM
-  static constexpr int KU = (X >> 4) & 15;     // 16-key groups in flight at once in a warp
-  static constexpr int SUB = X & 15;           // warps of a row group that share a block
-  static constexpr int THREADS = (W + 1) * 32;
-};
-template <int NT> struct I4Cfg : I4CfgT<HSWA_I4_CFG1> {};
-template <> struct I4Cfg<2> : I4CfgT<HSWA_I4_CFG2> {};
+// 4 consumer warps, two CTAs per SM, 32 keys of a warp in flight. Measured against (us, 256K-token sequence /
+// mixed batch with drafts, cold L2; here 78 / 655): 6 warps 78 / 1001 (its 128 registers spill), 8 warps in
+// one CTA 113 / 721, 12 warps 115 / 1014, 16 keys in flight 111 / 752, 64 keys 111 / 655.
+constexpr int I4_WARPS = 4;
+constexpr int I4_CTAS = 2;
+constexpr int I4_KU = 2;  // 16-key groups
+constexpr int I4_THREADS = (I4_WARPS + 1) * 32;
 
 // One work item as the producer hands it to the consumers.
 struct I4Item {
@@ -109,7 +95,6 @@ struct I4Item {
 
 template <int D, int NT, int RG>
 struct I4Smem {
-  using CFG = I4Cfg<NT>;
   static constexpr int ROWS = 8 * NT * RG;
   static constexpr int BLK = (int)i4_block_bytes(64, D);
   static constexpr int STAGE = 2 * BLK;
@@ -117,33 +102,28 @@ struct I4Smem {
   static constexpr int AREA_STRIDE = D + 4;  // floats
   static constexpr int Q_OFF = 0;
   static constexpr int AREA_OFF = Q_OFF + 2 * Q_BYTES;
-  static constexpr int AREAS = RG == 2 ? CFG::W / 2 : CFG::W;  // one per warp of a row group
+  static constexpr int AREAS = I4_WARPS / RG;  // one per warp of a row group
   static constexpr int ML_OFF = AREA_OFF + AREAS * ROWS * AREA_STRIDE * 4;
   // m, l, sum p lo per (warp, row), then per row
-  static constexpr int ROW_OFF = ML_OFF + (3 * CFG::W * ROWS + 3 * ROWS) * 4;  // per row: token, output offset
+  static constexpr int ROW_OFF = ML_OFF + (3 * I4_WARPS * ROWS + 3 * ROWS) * 4;  // per row: token, output offset
   static constexpr int ITEM_OFF = ROW_OFF + 2 * ROWS * 4;
   static constexpr int MAX_NS = 32;
   static constexpr int BAR_OFF = (ITEM_OFF + 2 * (int)sizeof(I4Item) + 15) / 16 * 16;
   static constexpr int STAGE_OFF = (BAR_OFF + (2 * MAX_NS + 5) * 8 + 16 + 127) / 128 * 128;
-  // as many blocks in flight as the shared memory of CTAS CTAs per SM allows
-  static constexpr int FIT = (227 * 1024 / CFG::CTAS - 1024 - STAGE_OFF) / STAGE;
+  // as many blocks in flight as the shared memory of I4_CTAS CTAs per SM allows
+  static constexpr int FIT = (227 * 1024 / I4_CTAS - 1024 - STAGE_OFF) / STAGE;
   static constexpr int NS = FIT < MAX_NS ? FIT : MAX_NS;
   static constexpr int BYTES = STAGE_OFF + NS * STAGE;
   static_assert(NS >= 4, "blocks in flight");
 };
 
 template <int D, int NT, int RG, bool MOD>
-__global__ void __launch_bounds__(I4Cfg<NT>::THREADS, I4Cfg<NT>::CTAS) decode_i4_kernel(DecParams p) {
+__global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParams p) {
   using SM = I4Smem<D, NT, RG>;
   constexpr int ROWS = SM::ROWS;
   constexpr int NS = SM::NS;
-  using CFG = I4Cfg<NT>;
-  constexpr int I4_WARPS = CFG::W;
   constexpr int KW = I4_WARPS / RG;    // warps that share a row group
-  constexpr int SUB = CFG::SUB;
-  constexpr int GW = 4 / SUB;          // 16-key groups of a block per warp
-  constexpr int KU = CFG::KU < GW ? CFG::KU : GW;
-  static_assert(KW % SUB == 0, "warps share blocks evenly");
+  constexpr int KU = I4_KU;
   constexpr int NW = D / 32;           // 32-bit words of K codes per lane
   constexpr int MT = D / 16;           // m-tiles of O^T
   extern __shared__ __align__(128) uint8_t smem[];
@@ -169,7 +149,7 @@ __global__ void __launch_bounds__(I4Cfg<NT>::THREADS, I4Cfg<NT>::CTAS) decode_i4
   }
   int* row_tok = reinterpret_cast<int*>(smem + SM::ROW_OFF);  // new token of a query row
   int* row_out = row_tok + ROWS;  // its place in the output, from (sequence, first token, first head of g)
-  for (int r = tid; r < ROWS; r += CFG::THREADS) {
+  for (int r = tid; r < ROWS; r += I4_THREADS) {
     const int t = r < p.R ? r / p.G : 0;
     row_tok[r] = t;
     row_out[r] = (t * p.Hq + (r - t * p.G)) * D;
@@ -177,7 +157,7 @@ __global__ void __launch_bounds__(I4Cfg<NT>::THREADS, I4Cfg<NT>::CTAS) decode_i4
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&full[i], 33);  // the producer's 32 lanes and its byte count
-      mbar_init(&empty[i], RG * SUB);  // the warps that read a block
+      mbar_init(&empty[i], RG);  // the warps that read a block
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&item_full[i], 1);
@@ -534,7 +514,7 @@ __global__ void __launch_bounds__(I4Cfg<NT>::THREADS, I4Cfg<NT>::CTAS) decode_i4
     uint32_t n_done = 0;     // blocks this warp has added to O
     const int lo_min = I.lo_min, lo_max = I.lo_max, hi_min = I.hi_min, hi_max = I.hi_max;
 
-    for (int kb = kw / SUB; kb < n_blk; kb += KW / SUB) {
+    for (int kb = kw; kb < n_blk; kb += KW) {
       const uint32_t cb = cnt + kb;
       const int st = cb % NS;
       if (!warp_wait(&full[st], (cb / NS) & 1, p.err)) return;
@@ -545,7 +525,7 @@ __global__ void __launch_bounds__(I4Cfg<NT>::THREADS, I4Cfg<NT>::CTAS) decode_i4
       const int kend = min(is_new ? L + p.n_qt : ib, hi_max);  // no key any row sees at or past this
       const bool edge = kbase + 64 > min(kend, hi_min) || kbase < lo_max;
 #pragma unroll 1
-      for (int k0 = (kw % SUB) * 16 * GW; k0 < (kw % SUB + 1) * 16 * GW; k0 += 16 * KU) {
+      for (int k0 = 0; k0 < 64; k0 += 16 * KU) {
         if (edge && (kbase + k0 >= kend || kbase + k0 + 16 * KU <= lo_min)) continue;  // nothing here
         // ---- S^T = K Q^T, KU groups of 16 keys
         float acc[KU][NT][4];

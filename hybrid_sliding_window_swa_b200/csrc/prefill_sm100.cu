@@ -405,13 +405,6 @@ __device__ __forceinline__ void zero_rows(uint8_t* dst, int kb, int kmin, int km
   }
 }
 
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
-
 // Rolling-buffer rows of one key tile with cp.async (general W and chunk start):
 // rows whose position is not held by the ring (or is negative) are zero-filled.
 template <int D, bool I4, bool MOD>
