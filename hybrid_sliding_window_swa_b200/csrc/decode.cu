@@ -1378,7 +1378,9 @@ int64_t ext_items_bound(int n_seqs, int Hkv, int64_t max_ctx_len) {
   const int64_t pairs = (int64_t)n_seqs * Hkv;
   const int64_t coarse = pairs * max_splits(0, max_ctx_len, SPLIT), fine = pairs * max_splits(0, max_ctx_len, 2048);
   const int64_t least = kExtCtas + pairs > fine ? kExtCtas + pairs : fine;
-  const int64_t cut = 4 * kExtCtas + pairs < least ? 4 * kExtCtas + pairs : least;
+  const int64_t finest = pairs * max_splits(0, max_ctx_len, 256);
+  int64_t cut = 4 * kExtCtas + pairs < least ? 4 * kExtCtas + pairs : least;
+  if (cut > finest) cut = finest;
   return coarse > cut ? coarse : cut;
 }
 
