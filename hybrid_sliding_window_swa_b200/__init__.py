@@ -343,6 +343,14 @@ class ScoreMod:
                          _ptr(self.key_begin, torch.int64, "key_begin"), _ptr(self.key_end, torch.int64, "key_end"))
 
 
+def _out_like(name: str, out: torch.Tensor | None, x: torch.Tensor) -> torch.Tensor:
+    if out is None:
+        return torch.empty_like(x)
+    if out.shape != x.shape or out.device != x.device:
+        raise ValueError(f"{name} must have the shape and device of its input")
+    return out
+
+
 def rope_fwd(rope: RopeDesc, q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor, q_out: torch.Tensor | None = None,
              k_out: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """Rotate q [..., Hq, d] and k [..., Hkv, d] of the same tokens by their positions pos
@@ -356,14 +364,7 @@ def rope_fwd(rope: RopeDesc, q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor
     n = math.prod(qs[:-2])
     if pos.shape[0] != rope.n_axes or pos.numel() != rope.n_axes * n:
         raise ValueError(f"pos must be [n_axes, tokens] = [{rope.n_axes}, {n}], got {tuple(pos.shape)}")
-    if q_out is None:
-        q_out = torch.empty_like(q)
-    elif q_out.shape != qs:
-        raise ValueError("q_out must have the shape of q")
-    if k_out is None:
-        k_out = torch.empty_like(k)
-    elif k_out.shape != ks:
-        raise ValueError("k_out must have the shape of k")
+    q_out, k_out = _out_like("q_out", q_out, q), _out_like("k_out", k_out, k)
     _check(load_library().rope_fwd(
         rope.c(), d, n, _ptr(pos, torch.int64, "pos"), _ptr(q, torch.bfloat16, "q"),
         _ptr(q_out, torch.bfloat16, "q_out"), qs[-2], _ptr(k, torch.bfloat16, "k"),
@@ -385,9 +386,9 @@ def kv_pool_append_rope(pool: KVPool, layer: int, rope: RopeDesc, q: torch.Tenso
         raise ValueError("q, k, v must be [n_seqs, n_tok, heads, head_dim] of the pool")
     if pos.shape[0] != rope.n_axes or pos.numel() != rope.n_axes * n_seqs * n_tok:
         raise ValueError(f"pos must be [n_axes, tokens] = [{rope.n_axes}, {n_seqs * n_tok}], got {tuple(pos.shape)}")
-    q_out = torch.empty_like(q) if q_out is None else q_out
-    if k_out is None and keys_out:
-        k_out = torch.empty_like(k)
+    q_out = _out_like("q_out", q_out, q)
+    if k_out is not None or keys_out:
+        k_out = _out_like("k_out", k_out, k)
     pt_stride = page_table.shape[1] if page_table is not None else 0
     _check(load_library().kv_pool_append_rope(
         pool.handle, layer, rope.c(), _ptr(pos, torch.int64, "pos"), n_seqs,

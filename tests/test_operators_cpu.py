@@ -96,6 +96,18 @@ def test_python_side_checks():
         hs.ScoreMod(dist_slope=torch.zeros(7)).c((2, 3), 8)
 
 
+def test_outputs_of_a_rotating_commit_have_the_shapes_of_their_inputs():
+    class Pool:
+        desc = hs.PoolDesc(1, 1, 128, 2, 64, 1, 1)
+        handle = None
+    rope, q, k = hs.RopeDesc((1.0,) * 8), torch.zeros(1, 3, 4, 64), torch.zeros(1, 3, 2, 64)
+    pos, start = torch.zeros(1, 3, dtype=torch.int64), torch.zeros(1, dtype=torch.int64)
+    for bad in (dict(q_out=torch.zeros(1, 3, 2, 64)), dict(k_out=torch.zeros(1, 2, 2, 64)),
+                dict(k_out=torch.zeros(1, 2, 2, 64), keys_out=False), dict(k_out=torch.zeros(1, 3, 2, 64, device="meta"))):
+        with pytest.raises(ValueError, match="shape and device"):
+            hs.kv_pool_append_rope(Pool, 1, rope, q, k, k, pos, start, **bad)
+
+
 def test_plain_attention_equals_torch():
     g = torch.Generator().manual_seed(1)
     q, k, v = (torch.randn(*s, generator=g, dtype=torch.float64) for s in ((5, 4, 64), (9, 2, 64), (9, 2, 64)))
