@@ -215,11 +215,6 @@ __device__ __forceinline__ int class_b(const DecParams& p, int s, int64_t L) {
   return c < NCLS_B - 1 ? c : NCLS_B - 1;
 }
 
-// Programmatic dependent launch: the launch may begin before its predecessor in the stream has finished;
-// grid_wait holds until that has, with its writes visible. grid_go lets the successor begin.
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 // Builds the work list (see PlanView) and resets the work counter. One block of 1024 threads:
 // class totals, then a stable placement chunk by chunk (warp ballots give each thread its rank
 // among earlier threads of its class), then prefix sums of the body splits in part-A order.
@@ -1241,22 +1236,6 @@ __global__ void __launch_bounds__(WPR == 1 ? 128 : WPR * 32) merge_rows_kernel(D
   uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (((int64_t)s * p.n_qt + t) * p.Hq + g * p.G + hh) * D + lane * V);
 #pragma unroll
   for (int v = 0; v < V; v += 2) dst[v / 2] = pack_bf16x2(acc[v] * iv, acc[v + 1] * iv);
-}
-
-// Launch with programmatic dependence on the launch before it in the stream.
-template <typename K>
-cudaError_t launch_dependent(K kernel, int grid, int block, size_t smem, cudaStream_t stream, const DecParams& p) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 template <int D>

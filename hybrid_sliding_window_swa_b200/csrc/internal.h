@@ -77,6 +77,22 @@ int launch_append(const hswa_pool* pool, int layer, int n_seqs, const int32_t* s
                   const int64_t* start_pos, int n_tok, const uint16_t* k, const uint16_t* v,
                   const int32_t* page_table, int pt_stride, cudaStream_t stream);
 
+// Launch with programmatic dependence on the launch before it in the stream.
+template <typename K, typename... A>
+inline cudaError_t launch_dependent(K kernel, int grid, int block, size_t smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // The destination of a commit into `layer`, as the commit kernels take it.
 void fill_commit_dst(const hswa_pool* pool, int layer, int n_tok, const int32_t* seq_ids, const int64_t* start_pos,
                      const int32_t* page_table, int pt_stride, struct CommitDst* out);

@@ -418,3 +418,32 @@ def test_a_request_from_prompt_to_tokens(fmt):
             ref.check(o[0], r, f"layer {layer} decode at {L}")
             hs.kv_pool_append(pool, layer, k[:, :1].contiguous(), v[:, :1].contiguous(), ctx, **kw)
     assert hs.hswa_pool_check_error(pool) == 0
+
+
+def test_calls_in_a_row_share_a_workspace_and_feed_each_other():
+    """Each call's output is the next one's queries; sizes on both sides of the one-launch key ranges."""
+    hq, hkv, d = 4, 2, 64
+    sizes = [150, 4500, 130, 900]
+    n = max(sizes)
+    per = (n + 63) // 64
+    pool = make_pool(BF, hkv, d, 0, 1, 64, 1, per)
+    pt = torch.arange(per, dtype=torch.int32).view(1, per).cuda()
+    zero = torch.tensor([0]).cuda()
+    hs.kv_pool_append(pool, 0, randn(1, 1, n, hkv, d).cuda(), randn(2, 1, n, hkv, d).cuda(), zero, page_table=pt)
+    q = randn(3, 1, n, hq, d).cuda()
+    mods = [hs.ScoreMod(key_begin=(torch.arange(m) // (20 + m // 7) * (20 + m // 7))[None].cuda()) for m in sizes]
+    ws = torch.empty(hs.prefill_mod_workspace_size(pool, 1, n), dtype=torch.uint8, device="cuda")
+
+    def chain(wait):
+        x = q.clone()
+        for _ in range(3):
+            for m, mod in zip(sizes, mods):
+                y = x.clone()
+                y[:, :m] = hs.full_prefill_mod_fwd(pool, 0, x[:, :m].contiguous(), pt, mod, ws, start_pos=zero)
+                x = y
+                if wait:
+                    torch.cuda.synchronize()
+        return x
+
+    assert torch.equal(chain(False), chain(True))
+    assert hs.hswa_pool_check_error(pool) == 0
