@@ -1304,22 +1304,22 @@ int launch_t(DecParams& p, int n_items_max, int sms, int64_t nsp_max, size_t mer
   return HSWA_OK;
 }
 
-template <int D, int NT, int RG, bool MOD>
+template <int D, int NT, int RG, bool MOD, bool SOLO>
 int launch_i4(DecParams& p, int n_items_max, int sms, int device, int64_t nsp_max, cudaStream_t stream) {
-  using SM = I4Smem<D, NT, RG>;
-  HSWA_SET_SMEM((decode_i4_kernel<D, NT, RG, MOD>), SM::BYTES, device);
+  using SM = I4Smem<D, NT, RG, SOLO>;
+  HSWA_SET_SMEM((decode_i4_kernel<D, NT, RG, MOD, SOLO>), SM::BYTES, device);
   int grid = sms * I4_CTAS;
   if (grid > n_items_max) grid = n_items_max;
   if (grid < 1) grid = 1;
   p.small = p.n_seqs <= 32 ? 1 : 0;
   cudaError_t e = cudaSuccess;
-  if (p.small) {
-    decode_i4_kernel<D, NT, RG, MOD><<<grid, I4_THREADS, SM::BYTES, stream>>>(p);
+  if (SOLO || p.small) {
+    decode_i4_kernel<D, NT, RG, MOD, SOLO><<<grid, I4_THREADS, SM::BYTES, stream>>>(p);
   } else {
     plan_kernel<true><<<1, 1024, 0, stream>>>(p);
-    e = launch_dependent(decode_i4_kernel<D, NT, RG, MOD>, grid, I4_THREADS, SM::BYTES, stream, p);
+    e = launch_dependent(decode_i4_kernel<D, NT, RG, MOD, SOLO>, grid, I4_THREADS, SM::BYTES, stream, p);
   }
-  if (e == cudaSuccess && nsp_max > 1) e = launch_merge_rows<D>(p, nsp_max, stream);
+  if (!SOLO && e == cudaSuccess && nsp_max > 1) e = launch_merge_rows<D>(p, nsp_max, stream);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) {
     set_error("hybrid_decode_fwd: launch failed: %s", cudaGetErrorString(e));
@@ -1457,12 +1457,16 @@ int launch_decode(const DecodeLaunch& Lc, cudaStream_t stream) {
   const size_t msm = decode_merge_smem_bytes(p.n_seqs, p.n_qt, p.Hq, p.Hkv, p.window, p.max_ctx_len);
   const int sms = pool->sms;
   if (pool->i4) {
-#define HSWA_I4(DD, MODD)                                                              \
-  (p.R <= 8    ? launch_i4<DD, 1, 1, MODD>(p, nmax, sms, pool->device, nsp_max, stream)  \
-   : p.R <= 16 ? launch_i4<DD, 2, 1, MODD>(p, nmax, sms, pool->device, nsp_max, stream)  \
-               : launch_i4<DD, 2, 2, MODD>(p, nmax, sms, pool->device, nsp_max, stream))
+    // short contexts and more items than the CTAs take at once: a team of warps per item
+    const bool solo = nsp_max == 1 && p.split <= 512 && mi > 2 * kExtCtas;
+#define HSWA_I4_R(DD, MODD, SOLO_)                                                                  \
+  (p.R <= 8    ? launch_i4<DD, 1, 1, MODD, SOLO_>(p, nmax, sms, pool->device, nsp_max, stream)  \
+   : p.R <= 16 ? launch_i4<DD, 2, 1, MODD, SOLO_>(p, nmax, sms, pool->device, nsp_max, stream)  \
+               : launch_i4<DD, 2, 2, MODD, SOLO_>(p, nmax, sms, pool->device, nsp_max, stream))
+#define HSWA_I4(DD, MODD) (solo ? HSWA_I4_R(DD, MODD, true) : HSWA_I4_R(DD, MODD, false))
     if (Lc.d == 128) return Lc.mod ? HSWA_I4(128, true) : HSWA_I4(128, false);
     return Lc.mod ? HSWA_I4(64, true) : HSWA_I4(64, false);
+#undef HSWA_I4_R
 #undef HSWA_I4
   }
   if (Lc.mod) {

@@ -88,28 +88,34 @@ struct I4Item {
   int a, b;              // cached keys [a, b) of this split
   int n_cached, n_blk;   // blocks of cached keys, blocks with the new tokens
   int nsp;               // splits of the sequence
+  uint32_t cnt0;         // blocks before its first one (their place in the stage ring)
   int lo_min, lo_max;    // over the rows: smallest and largest first visible position
   int hi_min, hi_max;    // smallest and largest end of the visible ranges
   int row_lo[8], row_hi[8];  // per new token
 };
 
-template <int D, int NT, int RG>
+// SOLO: items of at most 512 keys, one split each, of which there are many (the ring of a large batch). A team
+// of RG warps takes a whole item, its rows divided, so that no states are merged and the teams of a CTA do not
+// wait for one another; items are (sequence, KV head) in order, without a plan kernel.
+template <int D, int NT, int RG, bool SOLO>
 struct I4Smem {
   static constexpr int ROWS = 8 * NT * RG;
+  static constexpr int TEAMS = SOLO ? I4_WARPS / RG : 1;
+  static constexpr int SLOTS = 2 * TEAMS;  // items handed out ahead
   static constexpr int BLK = (int)i4_block_bytes(64, D);
   static constexpr int STAGE = 2 * BLK;
   static constexpr int Q_BYTES = ROWS * D * 2;
   static constexpr int AREA_STRIDE = D + 4;  // floats
   static constexpr int Q_OFF = 0;
-  static constexpr int AREA_OFF = Q_OFF + 2 * Q_BYTES;
-  static constexpr int AREAS = I4_WARPS / RG;  // one per warp of a row group
+  static constexpr int AREA_OFF = Q_OFF + SLOTS * Q_BYTES;
+  static constexpr int AREAS = SOLO ? 0 : I4_WARPS / RG;  // one per warp of a row group
   static constexpr int ML_OFF = AREA_OFF + AREAS * ROWS * AREA_STRIDE * 4;
   // m, l, sum p lo per (warp, row), then per row
-  static constexpr int ROW_OFF = ML_OFF + (3 * I4_WARPS * ROWS + 3 * ROWS) * 4;  // per row: token, output offset
+  static constexpr int ROW_OFF = ML_OFF + (SOLO ? 0 : (3 * I4_WARPS * ROWS + 3 * ROWS) * 4);  // per row: token, output offset
   static constexpr int ITEM_OFF = ROW_OFF + 2 * ROWS * 4;
   static constexpr int MAX_NS = 32;
-  static constexpr int BAR_OFF = (ITEM_OFF + 2 * (int)sizeof(I4Item) + 15) / 16 * 16;
-  static constexpr int STAGE_OFF = (BAR_OFF + (2 * MAX_NS + 5) * 8 + 16 + 127) / 128 * 128;
+  static constexpr int BAR_OFF = (ITEM_OFF + SLOTS * (int)sizeof(I4Item) + 15) / 16 * 16;
+  static constexpr int STAGE_OFF = (BAR_OFF + (2 * MAX_NS + 2 * SLOTS + 1) * 8 + 16 + 127) / 128 * 128;
   // as many blocks in flight as the shared memory of I4_CTAS CTAs per SM allows
   static constexpr int FIT = (227 * 1024 / I4_CTAS - 1024 - STAGE_OFF) / STAGE;
   static constexpr int NS = FIT < MAX_NS ? FIT : MAX_NS;
@@ -117,12 +123,13 @@ struct I4Smem {
   static_assert(NS >= 4, "blocks in flight");
 };
 
-template <int D, int NT, int RG, bool MOD>
+template <int D, int NT, int RG, bool MOD, bool SOLO>
 __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParams p) {
-  using SM = I4Smem<D, NT, RG>;
+  using SM = I4Smem<D, NT, RG, SOLO>;
   constexpr int ROWS = SM::ROWS;
   constexpr int NS = SM::NS;
-  constexpr int KW = I4_WARPS / RG;    // warps that share a row group
+  constexpr int SLOTS = SM::SLOTS, TEAMS = SM::TEAMS;
+  constexpr int KW = I4_WARPS / RG / TEAMS;  // warps that share an item's row group
   constexpr int KU = I4_KU;
   constexpr int NW = D / 32;           // 32-bit words of K codes per lane
   constexpr int MT = D / 16;           // m-tiles of O^T
@@ -130,17 +137,18 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::BAR_OFF);
   uint64_t* empty = full + SM::MAX_NS;
   uint64_t* item_full = empty + SM::MAX_NS;
-  uint64_t* item_empty = item_full + 2;
-  uint64_t* cons = item_empty + 2;
+  uint64_t* item_empty = item_full + SLOTS;
+  uint64_t* cons = item_empty + SLOTS;
   int* go = reinterpret_cast<int*>(cons + 1);
   I4Item* items = reinterpret_cast<I4Item*>(smem + SM::ITEM_OFF);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   WsHeader* hdr = reinterpret_cast<WsHeader*>(p.ws);
 
   // what the producer needs first is read before the barriers are set up
-  const int err0 = p.small && tid == 0 ? read_error(p.err) : 0;
+  const bool fixed = SOLO || p.small;  // items are worked out here, not read from a plan
+  const int err0 = fixed && tid == 0 ? read_error(p.err) : 0;
   int sp_L = 0, sp_body = 0, sp_excl = 0, sp_total = 0;
-  if (p.small && warp == I4_WARPS) {
+  if (!SOLO && p.small && warp == I4_WARPS) {
     const SmallPlan sp(p);
     sp_L = sp.L;
     sp_body = sp.body;
@@ -159,16 +167,16 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
       mbar_init(&full[i], 33);  // the producer's 32 lanes and its byte count
       mbar_init(&empty[i], RG);  // the warps that read a block
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < SLOTS; ++i) {
       mbar_init(&item_full[i], 1);
-      mbar_init(&item_empty[i], I4_WARPS);
+      mbar_init(&item_empty[i], I4_WARPS / TEAMS);
     }
     mbar_init(cons, I4_WARPS);
     fence_barrier_init();
   }
   grid_go();    // the merge may take its place; it waits for this grid's end before it reads
   grid_wait();  // the work list
-  if (tid == 0) *go = (p.small ? err0 : read_error(p.err)) == 0;
+  if (tid == 0) *go = (fixed ? err0 : read_error(p.err)) == 0;
   __syncthreads();
   if (!*go) return;  // a pending device error: skip the work
 
@@ -176,7 +184,10 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
     // ------------------------------------------------------------ producer
     const PlanView pv(p.ws, p.n_seqs);
     int total, body_total;
-    if (p.small) {
+    if constexpr (SOLO) {
+      body_total = 0;
+      total = p.n_seqs * p.Hkv;
+    } else if (p.small) {
       body_total = sp_total;
       total = (sp_total + p.n_seqs) * p.Hkv;
     } else {
@@ -184,13 +195,13 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
       total = hdr->total_items;
     }
     uint32_t cnt = 0;  // blocks issued
-    int it = 0;
+    int it = 0, ends = 0;
     bool ok = true;
     for (;; ++it) {
-      const int slot = it & 1;
-      if (!(ok = warp_wait(&item_empty[slot], ((it >> 1) & 1) ^ 1, p.err))) break;
+      const int slot = it % SLOTS;
+      if (!(ok = warp_wait(&item_empty[slot], ((it / SLOTS) & 1) ^ 1, p.err))) break;
       int item = 0;
-      if (p.small) {
+      if (fixed) {
         item = blockIdx.x + it * (int)gridDim.x;
       } else {
         if (lane == 0) item = atomicAdd(&hdr->counter, 1);
@@ -202,12 +213,18 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
           I.item = -1;
           mbar_arrive(&item_full[slot]);
         }
-        break;
+        if (++ends == TEAMS) break;  // every team has been told
+        continue;
       }
       const int g = item % p.Hkv;
       const int sc = item / p.Hkv;
       int s, c, L, nsp;
-      if (p.small) {
+      if constexpr (SOLO) {
+        s = sc;
+        c = 0;
+        L = (int)safe_len(p, s);
+        nsp = 1;
+      } else if (p.small) {
         if (sc < body_total) {
           // the last sequence whose prefix is not past sc (those without body splits share a prefix
           // with their successor)
@@ -231,7 +248,7 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
         s = pv.tail[sc - body_total];
         c = -1;
       }
-      if (!p.small) {
+      if (!fixed) {
         L = (int)safe_len(p, s);
         nsp = n_splits_x<true>(p, s, L);
       }
@@ -270,6 +287,7 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
         I.n_cached = n_cached;
         I.n_blk = n_blk;
         I.nsp = nsp;
+        I.cnt0 = cnt;
         I.lo_min = lo_min;
         I.lo_max = lo_max;
         I.hi_min = hi_min;
@@ -334,13 +352,16 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
               if (x >= p.window) x = p.window >= 64 ? x - p.window : x % p.window;
               return x;
             };
-            constexpr int CPR = D / 32;  // 16-byte chunks per row
-#pragma unroll 4
-            for (int i = lane; i < nvalid * CPR; i += 32) {
-              const int r = i / CPR, ch = i % CPR;
-              const int64_t off = (int64_t)wrap(r) * (D / 2) + ch * 16;
-              cp_async_16(smem_u32(ks) + i * 16, rk + off, 16);
-              cp_async_16(smem_u32(vs) + i * 16, rv + off, 16);
+            // codes: one run of slots, or two where the ring wraps (nvalid < W); pairs are 4-byte copies
+            if (lane == 0) {
+              const int n0 = min(nvalid, p.window - slot0);
+              mbar_arrive_expect_tx(&full[st], nvalid * D);  // K and V
+              bulk_load(ks, rk + (int64_t)slot0 * (D / 2), n0 * (D / 2), &full[st]);
+              bulk_load(vs, rv + (int64_t)slot0 * (D / 2), n0 * (D / 2), &full[st]);
+              if (n0 < nvalid) {
+                bulk_load(ks + n0 * (D / 2), rk, (nvalid - n0) * (D / 2), &full[st]);
+                bulk_load(vs + n0 * (D / 2), rv, (nvalid - n0) * (D / 2), &full[st]);
+              }
             }
             const int64_t pair0 = (int64_t)p.window * (D / 2);
             for (int r = lane; r < nvalid; r += 32) {
@@ -353,9 +374,9 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
               *i4_pair<D>(ks, 64, r) = 0u;
               *i4_pair<D>(vs, 64, r) = 0u;
             }
+            if (lane == 0) mbar_arrive(&full[st]);
           }
           fence_proxy_async_smem();
-          if (lane == 0) mbar_arrive(&full[st]);
           cp_async_arrive(&full[st]);
         } else {
           // the new tokens, as the cache will hold them: D / 8 lanes per row
@@ -400,8 +421,8 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
       // copies in flight must land before the CTA may end (bounded; the error word is already set)
       const uint32_t first = cnt > (uint32_t)NS ? cnt - NS : 0;
       for (uint32_t x = first; x < cnt; ++x) (void)mbar_wait_limit(&full[x % NS], (x / NS) & 1, nullptr, kWaitLimitNs);
-      for (int x = it > 1 ? it - 1 : 0; x <= it; ++x)
-        (void)mbar_wait_limit(&item_full[x & 1], (x >> 1) & 1, nullptr, 10000000ull);
+      for (int x = it >= SLOTS ? it - SLOTS + 1 : 0; x <= it; ++x)
+        (void)mbar_wait_limit(&item_full[x % SLOTS], (x / SLOTS) & 1, nullptr, 10000000ull);
     }
     return;
   }
@@ -409,7 +430,8 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
   // -------------------------------------------------------------- consumers
   const int g8 = lane >> 2, t4 = lane & 3;
   const int rg = RG == 2 ? warp & 1 : 0;
-  const int kw = RG == 2 ? warp >> 1 : warp;
+  const int pos = RG == 2 ? warp >> 1 : warp;
+  const int kw = SOLO ? 0 : pos;
   const int row0 = rg * 8 * NT;
   // key of S^T row g8 within a 16-key group (row g8 + 8: + 8), see the header comment
   const int pi0 = (g8 & 1) ? 4 + ((g8 >> 1) ^ 1) : g8 >> 1;
@@ -420,18 +442,19 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
   float* l_all = m_all + ROWS;
   float* b_all = l_all + ROWS;
   float* area = reinterpret_cast<float*>(smem + SM::AREA_OFF);  // [2][ROWS][AREA_STRIDE]
-  uint32_t cnt = 0, ncons = 0;
+  uint32_t ncons = 0;
   auto cons_sync = [&]() -> bool {
     __syncwarp();
     if (lane == 0) mbar_arrive(cons);
     return warp_wait(cons, (ncons++) & 1, p.err);
   };
 
-  for (int it = 0;; ++it) {
-    const int slot = it & 1;
-    if (!warp_wait(&item_full[slot], (it >> 1) & 1, p.err)) return;
+  for (int it = SOLO ? pos : 0;; it += TEAMS) {
+    const int slot = it % SLOTS;
+    if (!warp_wait(&item_full[slot], (it / SLOTS) & 1, p.err)) return;
     const I4Item& I = items[slot];
     if (I.item < 0) return;
+    const uint32_t cnt = I.cnt0;
     const int L = I.L, ia = I.a, ib = I.b, n_cached = I.n_cached, n_blk = I.n_blk;
 
     // ---- Q fragments: lane (g8, t4) holds dims [t4 D/4, +D/4) of row g8 of each n-tile
@@ -753,8 +776,6 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
     }
-    cnt += n_blk;
-
     // ---- merge the warps' states
     const int s = I.s, hg = I.g, nsp = I.nsp, item = I.item;
 #pragma unroll
@@ -766,6 +787,31 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
           l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], x);
           bs[nt][c] += __shfl_xor_sync(0xffffffffu, bs[nt][c], x);
         }
+    if constexpr (SOLO) {
+      // the whole row is here: lane (g8, t4) holds dims [g8 D/8, +D/8) of rows 2 t4 and 2 t4 + 1
+      uint16_t* out = p.o + ((int64_t)s * p.n_qt * p.Hq + hg * p.G) * D;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int r = row0 + nt * 8 + 2 * t4 + c;
+          const float inv = l[nt][c] == 0.f ? 0.f : 1.f / l[nt][c];  // (a row that sees nothing: 0)
+          const float fo = pow2i(e_cur), b0 = bs[nt][c];
+          uint32_t w[MT];
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+            w[i] = pack_bf16x2(fmaf(o[i][nt][c] * fo, 16777216.f, b0) * inv,
+                               fmaf(o[i][nt][2 + c] * fo, 1048576.f, b0) * inv);
+          if (r < p.R) {
+            uint4* dst = reinterpret_cast<uint4*>(out + row_out[r] + g8 * (D / 8));
+#pragma unroll
+            for (int i = 0; i < MT; i += 4) dst[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+          }
+        }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&item_empty[slot]);
+      continue;
+    }
     if (it > 0 && !cons_sync()) return;  // the previous item's output has been read
     if (lane == 0) mbar_arrive(&item_empty[slot]);
     if (g8 == 0) {

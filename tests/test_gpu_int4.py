@@ -168,6 +168,22 @@ def test_decode_of_more_sequences_than_a_warp():
         ref.check(o[b], r, f"ring seq {b} L={lens[b]}")
 
 
+# many short contexts, more items (sequences x KV heads) than the CTAs take at once, several to a team of warps
+@pytest.mark.parametrize("W,longest,n,n_qt,hq,hkv,d", [
+    (128, 5000, 100, 8, 64, 16, 128),   # 32 rows, two warps a team; rings that wrap
+    (100, 300, 90, 1, 64, 32, 64),      # 2 rows, one warp a team
+    (512, 2000, 80, 3, 32, 8, 128),     # 12 rows, contexts up to the longest that are not split
+    (3, 50, 75, 7, 24, 8, 64),          # 21 rows, a ring smaller than a page
+    (0, 500, 100, 1, 32, 16, 128),      # pages; tails inside a page
+    (0, 63, 76, 4, 64, 8, 64),          # at most one page
+    (0, 512, 75, 2, 64, 8, 128)])
+def test_decode_of_many_short_contexts(W, longest, n, n_qt, hq, hkv, d):
+    lens = [0, 1, longest, longest - 1] + [(41 * i * i + 13 * i) % (longest + 1) for i in range(n - 4)]
+    o, refs = decode_case(23, lens, n_qt, hq, hkv, d, W)
+    for b, r in enumerate(refs):
+        ref.check(o[b], r, f"W={W} seq {b} L={lens[b]}")
+
+
 @pytest.mark.parametrize("spread,q_scale", [(1e-4, 3e3), (300.0, 3e-3), (1e4, 1e-4), (1e-20, 1e20)])
 def test_decode_range_of_values(spread, q_scale):
     # scores of ordinary size from entries far from 1: the f16 operands are scaled per row and per step

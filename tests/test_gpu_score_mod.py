@@ -238,6 +238,13 @@ def test_decode(fmt, cap, bias, mask, lens, n_qt, hq, hkv, d, W):
     decode_case(fmt, lens, n_qt, hq, hkv, d, W, cap, bias, mask)
 
 
+@pytest.mark.parametrize("cap,bias,mask", [(20.0, True, "none"), (0.0, False, "docs"), (5.0, False, "wild"),
+                                           (0.0, True, "pad")])
+@pytest.mark.parametrize("n_qt,hq,hkv,d,W", [(4, 64, 8, 128, 100), (2, 16, 8, 64, 0)])
+def test_decode_of_many_short_4bit_contexts(cap, bias, mask, n_qt, hq, hkv, d, W):
+    decode_case(I4, [0, 1, 400] + [(53 * i * i + 7 * i) % 400 for i in range(75)], n_qt, hq, hkv, d, W, cap, bias, mask)
+
+
 @pytest.mark.parametrize("fmt", [BF, F8, I4])
 def test_padded_new_tokens_may_hold_anything(fmt):
     # rows 2 and 3 of a step are padding: they see nothing, nothing sees them, their k and v are NaN
