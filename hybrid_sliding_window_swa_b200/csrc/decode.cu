@@ -1457,8 +1457,13 @@ int launch_decode(const DecodeLaunch& Lc, cudaStream_t stream) {
   const size_t msm = decode_merge_smem_bytes(p.n_seqs, p.n_qt, p.Hq, p.Hkv, p.window, p.max_ctx_len);
   const int sms = pool->sms;
   if (pool->i4) {
-    // short contexts and more items than the CTAs take at once: a team of warps per item
-    const bool solo = nsp_max == 1 && p.split <= 512 && mi > 2 * kExtCtas;
+    // Short contexts and many items: a team of warps per item. Measured (us a call, 4 warps per item / a team;
+    // d = 128, 8 KV heads): 296 sequence-heads of 128 keys x 32 rows 19.1 / 14.5, 2048 of them 75.6 / 53.4; 384 keys
+    // x 32 rows 24.0 / 23.9 and 120 / 105, x 16 rows 19.1 / 19.2 and 84.9 / 78.9; 512 keys x 16 rows 95 / 110, x 8
+    // rows 16.4 / 14.9 and 66.3 / 63.0. With up to 32 sequences the other way has no plan kernel either and wins
+    // with few items (256 of 128 keys x 32 rows: 12.7 / 14.2).
+    const int64_t longest = p.window > 0 && p.max_ctx_len >= p.window ? p.window - 1 : p.max_ctx_len;
+    const bool solo = longest <= (p.R <= 8 ? 512 : 384) && mi > (p.n_seqs > 32 ? 256 : 2 * kExtCtas);
 #define HSWA_I4_R(DD, MODD, SOLO_)                                                                  \
   (p.R <= 8    ? launch_i4<DD, 1, 1, MODD, SOLO_>(p, nmax, sms, pool->device, nsp_max, stream)  \
    : p.R <= 16 ? launch_i4<DD, 2, 1, MODD, SOLO_>(p, nmax, sms, pool->device, nsp_max, stream)  \

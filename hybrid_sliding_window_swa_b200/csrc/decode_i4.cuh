@@ -94,7 +94,8 @@ struct I4Item {
   int row_lo[8], row_hi[8];  // per new token
 };
 
-// SOLO: items of at most 512 keys, one split each, of which there are many (the ring of a large batch). A team
+// SOLO: many short items of one split each (the ring of a large batch), where most of an item's ~9.5 us went into
+// its hand-over, the merge of the warps' states and the waits of warps without a block. A team
 // of RG warps takes a whole item, its rows divided, so that no states are merged and the teams of a CTA do not
 // wait for one another; items are (sequence, KV head) in order, without a plan kernel.
 template <int D, int NT, int RG, bool SOLO>
