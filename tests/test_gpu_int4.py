@@ -249,6 +249,33 @@ def test_bad_page_and_ring_row_are_reported():
     assert (pool.data == 0).all()
 
 
+def test_a_bad_ring_row_among_many_leaves_the_others_right():
+    n, hkv, hq, d, W, n_qt = 90, 8, 32, 64, 100, 4
+    pool = make_pool(hkv, d, 1, 0, W, n, 1)
+    ids = torch.arange(n, dtype=torch.int32, device="cuda")
+    start = torch.zeros(n, dtype=torch.int64, device="cuda")
+    k, v = rows(1, n * 150, hkv, d).view(n, 150, hkv, d).cuda(), rows(2, n * 150, hkv, d).view(n, 150, hkv, d).cuda()
+    hs.kv_pool_append(pool, 0, k, v, start, seq_ids=ids)
+    q = rows(3, n * n_qt, hq, d).view(n, n_qt, hq, d).cuda()
+    ws = torch.empty(hs.hybrid_decode_workspace_size(pool, n, n_qt, hq, 150), dtype=torch.uint8, device="cuda")
+    args = (pool, 0, q, k[:, :n_qt].contiguous(), v[:, :n_qt].contiguous(), start + 150, 150, ws)
+    good = hs.hybrid_decode_fwd(*args, seq_ids=ids)
+    assert hs.hswa_pool_check_error(pool) == 0
+    wrong = ids.clone()
+    wrong[37], wrong[80] = n, -1
+    o = torch.empty_like(q)
+    hs.hybrid_decode_fwd(*args, seq_ids=wrong, o=o)
+    assert hs.hswa_pool_check_error(pool) == hs.HSWA_ERR_DEVICE_BOUNDS
+    keep = [b for b in range(n) if b not in (37, 80)]
+    assert torch.equal(o[keep], good[keep])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        hs.hybrid_decode_fwd(*args, seq_ids=wrong, o=o)
+    wrong.copy_(ids)
+    g.replay()
+    assert hs.hswa_pool_check_error(pool) == 0 and torch.equal(o, good)
+
+
 def test_a_workspace_serves_every_smaller_call():
     hq, hkv, d, big = 4, 1, 64, 8192
     pool = make_pool(hkv, d, 0, 1, 1, 1, 130)
