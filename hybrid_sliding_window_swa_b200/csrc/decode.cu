@@ -26,6 +26,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "kv_quant.cuh"
+#include "stage_ring.h"
 
 namespace hswa {
 

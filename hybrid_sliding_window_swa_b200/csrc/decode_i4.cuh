@@ -38,7 +38,8 @@
 // producer also hands over the item's geometry and its Q rows. The warps take blocks in turn (for more
 // than 16 rows in pairs, half the rows each), 32 keys at a time so that enough independent MMAs are
 // in flight, and merge their softmax states at the end of the item.
-// Waits are bounded; a failing wait makes its warp return and the others run out theirs.
+// A stage is read by whichever warp its block falls to, so a block is awaited only once it has been issued
+// (stage_ring.h). Waits are bounded; a failing wait makes its warp return and the others run out theirs.
 
 __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
@@ -69,6 +70,32 @@ __device__ __forceinline__ void mma_f16_zero(float (&c)[4], uint32_t a0, uint32_
       "{%10,%10,%10,%10};"
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// The count of issued blocks (stage_ring.h), written by the producer and read by the consumers.
+__device__ __forceinline__ void set_issued(uint32_t* word, uint32_t n) {
+  asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(smem_u32(word)), "r"(n) : "memory");
+}
+__device__ __forceinline__ uint32_t get_issued(const uint32_t* word) {
+  uint32_t n;
+  asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(n) : "r"(smem_u32(word)) : "memory");
+  return n;
+}
+
+// Wait (bounded, the whole warp) until `block` has been issued; `seen` is the count last read.
+template <int NS>
+__device__ __forceinline__ bool wait_issued(const uint32_t* word, uint32_t block, uint32_t& seen, int* err) {
+  if (StageRing<NS>::may_wait(seen, block)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    seen = __shfl_sync(0xffffffffu, get_issued(word), 0);
+    if (StageRing<NS>::may_wait(seen, block)) return true;
+    if ((it & 255u) == 0) {
+      const bool late = globaltimer_ns() - t0 > kWaitLimitNs;
+      if (late) record_error(err, HSWA_ERR_TIMEOUT);
+      if (__any_sync(0xffffffffu, late || read_error(err) != 0)) return false;
+    }
+  }
 }
 
 // 2^e for -126 <= e <= 127.
@@ -122,6 +149,7 @@ struct I4Smem {
   static constexpr int NS = FIT < MAX_NS ? FIT : MAX_NS;
   static constexpr int BYTES = STAGE_OFF + NS * STAGE;
   static_assert(NS >= 4, "blocks in flight");
+  using Ring = StageRing<NS>;
 };
 
 template <int D, int NT, int RG, bool MOD, bool SOLO>
@@ -130,6 +158,7 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
   constexpr int ROWS = SM::ROWS;
   constexpr int NS = SM::NS;
   constexpr int SLOTS = SM::SLOTS, TEAMS = SM::TEAMS;
+  using Ring = typename SM::Ring;
   constexpr int KW = I4_WARPS / RG / TEAMS;  // warps that share an item's row group
   constexpr int KU = I4_KU;
   constexpr int NW = D / 32;           // 32-bit words of K codes per lane
@@ -141,6 +170,7 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
   uint64_t* item_empty = item_full + SLOTS;
   uint64_t* cons = item_empty + SLOTS;
   int* go = reinterpret_cast<int*>(cons + 1);
+  uint32_t* issued = reinterpret_cast<uint32_t*>(go + 1);  // blocks issued, see stage_ring.h
   I4Item* items = reinterpret_cast<I4Item*>(smem + SM::ITEM_OFF);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   WsHeader* hdr = reinterpret_cast<WsHeader*>(p.ws);
@@ -173,6 +203,7 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
       mbar_init(&item_empty[i], I4_WARPS / TEAMS);
     }
     mbar_init(cons, I4_WARPS);
+    *issued = 0;
     fence_barrier_init();
   }
   grid_go();    // the merge may take its place; it waits for this grid's end before it reads
@@ -313,12 +344,13 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
       const int32_t* pt_row = p.page_table ? p.page_table + (int64_t)s * p.pt_stride : nullptr;
       int my_page = -1;
       for (int kb = 0; kb < n_blk; ++kb, ++cnt) {
-        const int st = cnt % NS;
+        const int st = Ring::stage(cnt);
         if (p.window <= 0 && (kb & 31) == 0) {
           const int lp = (a >> 6) + kb + lane;
           my_page = kb + lane < n_cached && lp < p.pt_stride ? pt_row[lp] : -1;
         }
-        if (!(ok = warp_wait(&empty[st], ((cnt / NS) & 1) ^ 1, p.err))) break;
+        if (!(ok = warp_wait(&empty[st], Ring::parity(cnt) ^ 1, p.err))) break;
+        if (lane == 0) set_issued(issued, cnt + 1);
         uint8_t* ks = smem + SM::STAGE_OFF + st * SM::STAGE;
         uint8_t* vs = ks + SM::BLK;
         if (kb < n_cached && p.window <= 0) {
@@ -421,7 +453,7 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
     if (!ok) {
       // copies in flight must land before the CTA may end (bounded; the error word is already set)
       const uint32_t first = cnt > (uint32_t)NS ? cnt - NS : 0;
-      for (uint32_t x = first; x < cnt; ++x) (void)mbar_wait_limit(&full[x % NS], (x / NS) & 1, nullptr, kWaitLimitNs);
+      for (uint32_t x = first; x < cnt; ++x) (void)mbar_wait_limit(&full[Ring::stage(x)], Ring::parity(x), nullptr, kWaitLimitNs);
       for (int x = it >= SLOTS ? it - SLOTS + 1 : 0; x <= it; ++x)
         (void)mbar_wait_limit(&item_full[x % SLOTS], (x / SLOTS) & 1, nullptr, 10000000ull);
     }
@@ -444,6 +476,7 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
   float* b_all = l_all + ROWS;
   float* area = reinterpret_cast<float*>(smem + SM::AREA_OFF);  // [2][ROWS][AREA_STRIDE]
   uint32_t ncons = 0;
+  uint32_t n_issued = 0;  // as last read
   auto cons_sync = [&]() -> bool {
     __syncwarp();
     if (lane == 0) mbar_arrive(cons);
@@ -540,8 +573,8 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
 
     for (int kb = kw; kb < n_blk; kb += KW) {
       const uint32_t cb = cnt + kb;
-      const int st = cb % NS;
-      if (!warp_wait(&full[st], (cb / NS) & 1, p.err)) return;
+      const int st = Ring::stage(cb);
+      if (!wait_issued<NS>(issued, cb, n_issued, p.err) || !warp_wait(&full[st], Ring::parity(cb), p.err)) return;
       uint8_t* ks = smem + SM::STAGE_OFF + st * SM::STAGE;
       uint8_t* vs = ks + SM::BLK;
       const bool is_new = kb >= n_cached;
