@@ -13,7 +13,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["hswa_abi.cu", "pool_kernels.cu", "prefill_sm100.cu", "prefill_narrow.cu", "decode.cu",
            "rope.cu", "prefix_tree.cpp", "shard.cpp"]
 HEADERS = ["common.cuh", "internal.h", "prefill_tile.cuh", "decode_tc.cuh", "decode_i4.cuh",
-           "kv_quant.cuh", "kv_place.cuh", "stage_ring.h"]
+           "kv_quant.cuh", "kv_place.cuh", "stage_ring.h", "decode_split.h"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = [

@@ -24,6 +24,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "decode_split.h"
 #include "internal.h"
 #include "kv_quant.cuh"
 #include "stage_ring.h"
@@ -36,11 +37,6 @@ constexpr int DEC_THREADS = 128;
 constexpr int KB = 64;          // keys per block
 constexpr int NST = 3;          // pipeline stages (bf16 blocks)
 constexpr int NST8 = 6;         // pipeline stages (FP8 blocks: half the bytes, the same bytes in flight)
-#ifndef HSWA_DECODE_SPLIT
-#define HSWA_DECODE_SPLIT 8192
-#endif
-constexpr int SPLIT = HSWA_DECODE_SPLIT;  // cached keys per split (tuning parameter, multiple of KB)
-static_assert(SPLIT % 64 == 0, "splits start on page boundaries");
 
 struct WsHeader {
   int counter;
@@ -1249,36 +1245,6 @@ cudaError_t launch_merge_rows(const DecParams& p, int64_t max_splits, cudaStream
 #include "decode_tc.cuh"
 #include "decode_i4.cuh"
 
-// Largest split count of any sequence for these arguments.
-int64_t max_splits(int window, int64_t max_ctx_len, int split = SPLIT) {
-  const int64_t cached = window > 0 ? (max_ctx_len < window ? max_ctx_len : window - 1) : max_ctx_len;
-  const int64_t nsp = (cached + split - 1) / split;
-  return nsp < 1 ? 1 : nsp;
-}
-
-// Keys per split of an extended launch, from the sizes the host knows. One sequence: as many equal splits as
-// fill the resident CTAs once (a second round would pay the start and the merge of an item again: 104 us
-// against 89 us for 256K tokens). Several sequences, whose lengths may differ: about four items per CTA if
-// all were of the largest length, but at least 2048 keys (an item costs some 4 us besides its reads) unless
-// one round would not be full. At most 8192 keys, as in the other launches.
-constexpr int64_t kExtCtas = 296;  // two CTAs on each of 148 SMs
-int ext_split(int n_seqs, int Hkv, int window, int64_t max_ctx_len) {
-  const int64_t cached = window > 0 && max_ctx_len > window ? window : max_ctx_len;
-  const int64_t pairs = (int64_t)n_seqs * Hkv > 0 ? (int64_t)n_seqs * Hkv : 1;
-  auto cut = [&](int64_t n) { return (cached + n - 1) / n; };
-  int64_t split = cut(kExtCtas / pairs > 1 ? kExtCtas / pairs : 1);
-  if (n_seqs > 1) {
-    const int64_t fine = cut((4 * kExtCtas + pairs - 1) / pairs);
-    const int64_t least = split < 2048 ? split : 2048;
-    split = fine > least ? fine : least;
-  }
-  // a context of a few pages is one split: its 4 warps walk 8 blocks in less than a merge and its launch
-  // take (400 keys: 10.2 us a call against 12.3 with splits of 256; 613 keys: 12.3 against 11.7)
-  if (cached <= 512) return 512;
-  split = (split + 63) / 64 * 64;
-  return (int)(split < 256 ? 256 : (split > SPLIT ? SPLIT : split));
-}
-
 template <int D, int MT, bool FP8, bool EXT>
 int launch_t(DecParams& p, int n_items_max, int sms, int64_t nsp_max, size_t merge_smem, cudaStream_t stream) {
   using SM = DecSmem<D, MT, FP8>;
@@ -1350,19 +1316,6 @@ int launch_tc(DecParams& p, int n_items_max, int sms, size_t merge_smem, cudaStr
 }
 
 }  // namespace
-
-// What hybrid_decode_workspace_size promises for extended launches: at least the items of any call with at
-// most these sequences and this context length, and growing with both (the exact count need not: fewer
-// sequences may be cut finer).
-int64_t ext_items_bound(int n_seqs, int Hkv, int64_t max_ctx_len) {
-  const int64_t pairs = (int64_t)n_seqs * Hkv;
-  const int64_t coarse = pairs * max_splits(0, max_ctx_len, SPLIT), fine = pairs * max_splits(0, max_ctx_len, 2048);
-  const int64_t least = kExtCtas + pairs > fine ? kExtCtas + pairs : fine;
-  const int64_t finest = pairs * max_splits(0, max_ctx_len, 256);
-  int64_t cut = 4 * kExtCtas + pairs < least ? 4 * kExtCtas + pairs : least;
-  if (cut > finest) cut = finest;
-  return coarse > cut ? coarse : cut;
-}
 
 size_t decode_workspace_bound(int n_seqs, int n_qt, int Hq, int Hkv, int d, int64_t max_ctx_len) {
   WsLayout a(n_seqs, n_qt * (Hq / Hkv), d, (int64_t)n_seqs * Hkv * max_splits(0, max_ctx_len));
@@ -1458,13 +1411,7 @@ int launch_decode(const DecodeLaunch& Lc, cudaStream_t stream) {
   const size_t msm = decode_merge_smem_bytes(p.n_seqs, p.n_qt, p.Hq, p.Hkv, p.window, p.max_ctx_len);
   const int sms = pool->sms;
   if (pool->i4) {
-    // Short contexts and many items: a team of warps per item. Measured (us a call, 4 warps per item / a team;
-    // d = 128, 8 KV heads): 296 sequence-heads of 128 keys x 32 rows 19.1 / 14.5, 2048 of them 75.6 / 53.4; 384 keys
-    // x 32 rows 24.0 / 23.9 and 120 / 105, x 16 rows 19.1 / 19.2 and 84.9 / 78.9; 512 keys x 16 rows 95 / 110, x 8
-    // rows 16.4 / 14.9 and 66.3 / 63.0. With up to 32 sequences the other way has no plan kernel either and wins
-    // with few items (256 of 128 keys x 32 rows: 12.7 / 14.2).
-    const int64_t longest = p.window > 0 && p.max_ctx_len >= p.window ? p.window - 1 : p.max_ctx_len;
-    const bool solo = longest <= (p.R <= 8 ? 512 : 384) && mi > (p.n_seqs > 32 ? 256 : 2 * kExtCtas);
+    const bool solo = i4_teams(p.n_seqs, p.Hkv, p.R, p.window, p.max_ctx_len);  // a team of warps per item
 #define HSWA_I4_R(DD, MODD, SOLO_)                                                                  \
   (p.R <= 8    ? launch_i4<DD, 1, 1, MODD, SOLO_>(p, nmax, sms, pool->device, nsp_max, stream)  \
    : p.R <= 16 ? launch_i4<DD, 2, 1, MODD, SOLO_>(p, nmax, sms, pool->device, nsp_max, stream)  \
