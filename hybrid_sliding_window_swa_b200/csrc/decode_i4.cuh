@@ -551,7 +551,8 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
     }
 
     float o[MT][NT][4];
-    float m[NT][2], l[NT][2], bs[NT][2], l_sh[NT][2];
+    float m[NT][2], l[NT][2], bs[NT][2];
+    float ws[NT][2];  // sum of the weights as V takes them (p step 2^-e_cur) since they last left O, see below
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -559,7 +560,7 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
         m[nt][c] = -INFINITY;
         l[nt][c] = 0.f;
         bs[nt][c] = 0.f;
-        l_sh[nt][c] = 0.f;
+        ws[nt][c] = 0.f;
       }
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -711,8 +712,8 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
               m[nt][c] = mn;
               l[nt][c] *= al;
               bs[nt][c] *= al;
-              l_sh[nt][c] *= al;
               const float f = al * osc;
+              ws[nt][c] *= f;
 #pragma unroll
               for (int i = 0; i < MT; ++i) {
                 o[i][nt][c] *= f;
@@ -734,15 +735,24 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float w[4];
+            // the two rows of a lane together (packed operations: half the instructions)
+            uint64_t l2 = f2_pack(l[nt][0], l[nt][1]), b2 = f2_pack(bs[nt][0], bs[nt][1]);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const int k = x >> 1, c = x & 1;
-              const float e =
-                  ex2_approx(MOD ? acc[u][nt][x] - moff[nt][c] : fmaf(acc[u][nt][x], c1[nt][c], -moff[nt][c]));
-              l[nt][c] += e;
-              bs[nt][c] = fmaf(e, vlf[k], bs[nt][c]);
-              w[x] = e * vsf[k];
+            for (int k = 0; k < 2; ++k) {
+              float e[2];
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                e[c] = ex2_approx(MOD ? acc[u][nt][2 * k + c] - moff[nt][c]
+                                      : fmaf(acc[u][nt][2 * k + c], c1[nt][c], -moff[nt][c]));
+              const uint64_t e2 = f2_pack(e[0], e[1]);
+              l2 = f2_add(l2, e2);
+              b2 = f2_fma(e2, f2_pack(vlf[k], vlf[k]), b2);
+              const uint64_t w2 = f2_mul(e2, f2_pack(vsf[k], vsf[k]));
+              f2_unpack(w2, w[2 * k], w[2 * k + 1]);
+              if constexpr (!SOLO) f2_unpack(f2_add(f2_pack(ws[nt][0], ws[nt][1]), w2), ws[nt][0], ws[nt][1]);
             }
+            f2_unpack(l2, l[nt][0], l[nt][1]);
+            f2_unpack(b2, bs[nt][0], bs[nt][1]);
             pb[nt][0] = movmatrix_t(pack_f16x2(w[0], w[1]));
             pb[nt][1] = movmatrix_t(pack_f16x2(w[2], w[3]));
           }
@@ -781,31 +791,30 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
             }
         }
       }
-      // Every 4 blocks, move the codes' mean out of O: sum P c is 7.5 step sum p plus a small rest, and the
+      // Every 4 blocks, move the codes' mean out of O: sum P c is 7.5 sum p step plus a small rest, and the
       // tensor core's accumulation truncates, so over thousands of keys the rest (all that is left after
       // sum p lo is added) lost 0.2% of its size to the large common part. Any S may be taken from O as long
-      // as the same S is added to sum p lo; S = 7.5 (some key's step) (sum p since the last time).
-      if ((++n_done & 3u) == 0) {
-        const float sbar = __shfl_sync(0xffffffffu, __uint_as_float(*i4_pair<D>(vs, 64, 0) << 16), 0);
-        if (!is_new && sbar > 0.f) {
+      // as the same S is added to sum p lo; S = 7.5 (sum p step since the last time), the rows' own weights: a
+      // step of which a row sees little (a far larger V row of weight 0) must not enter its O. (A team's contexts
+      // of at most 512 keys stay below 2^-17 of the sum without that: 32 accumulations.)
+      if (!SOLO && (++n_done & 3u) == 0) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              float d = l[nt][c] - l_sh[nt][c];
-              l_sh[nt][c] = l[nt][c];
+          for (int c = 0; c < 2; ++c) {
+            float d = ws[nt][c];
+            ws[nt][c] = 0.f;
 #pragma unroll
-              for (int x = 4; x < 32; x <<= 1) d += __shfl_xor_sync(0xffffffffu, d, x);
-              const float S = 7.5f * sbar * d;
-              bs[nt][c] += 0.125f * S;  // the 8 lanes of a row are summed at the end
-              const float se = S * fe * 5.9604645e-8f, so = S * fe * 9.5367432e-7f;  // 2^-24, 2^-20
+            for (int x = 4; x < 32; x <<= 1) d += __shfl_xor_sync(0xffffffffu, d, x);
+            const float S = 7.5f * d;
+            bs[nt][c] = fmaf(0.125f * S, pow2i(e_cur), bs[nt][c]);  // the 8 lanes of a row are summed at the end
+            const float se = S * 5.9604645e-8f, so = S * 9.5367432e-7f;  // 2^-24, 2^-20
 #pragma unroll
-              for (int i = 0; i < MT; ++i) {
-                o[i][nt][c] -= se;
-                o[i][nt][2 + c] -= so;
-              }
+            for (int i = 0; i < MT; ++i) {
+              o[i][nt][c] -= se;
+              o[i][nt][2 + c] -= so;
             }
-        }
+          }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
