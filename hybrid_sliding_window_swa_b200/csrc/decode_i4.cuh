@@ -22,10 +22,13 @@
 //      rows).
 // P (times the key's V step) is rounded to f16 (11 bits; an fp32 sum keeps l and sum p lo) and turned
 // from accumulator to operand layout by movmatrix.
-// f16 range: Q is staged with its row maximum at 2^14 .. 2^15 and the factor kept in fp32. p is at most
-// 2^8 (lazy rescaling as in the other kernels) and the V steps are divided by a power of two that
-// brings the largest so far to 2^6 .. 2^7; a larger one raises it and rescales O. P keeps its 11 bits
-// down to 2^-20 of the largest p * step.
+// f16 range: Q is staged with its row maximum at 2^14 .. 2^15 and the factor kept in fp32. The weights are
+// p = 2^(z - off), where each query row's offset, a whole number, is held so that p step stays below 2^15: it moves
+// when that might be passed, to the place where the largest p step is at most 2^7, and l, sum p lo and O are
+// rescaled (O, l and sum p lo carry the same factor, which cancels in the end). Only keys that the row sees count:
+// another token of the step may see values of any size. P keeps its 11 bits down to 2^-21 of the row's largest
+// p step (for V steps of 2^-89 to 2^100; beyond them the small weights leave the fp32 or the f16 range). A minimum
+// counts as a step of 2^-20 of its size, and a step as at least 2^-89, which keeps sum p lo and l finite.
 //
 // What bounds it. 2 (d / 2 + 4) bytes per key and KV head. Up to 8 rows the reads do: 5.2 TB/s while the items
 // of a 256K-token sequence run (72 us the call; its 285 MB take 43 us). With 32 rows the instruction dispatch
@@ -101,6 +104,12 @@ __device__ __forceinline__ bool wait_issued(const uint32_t* word, uint32_t block
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 
+// What a row's (step, minimum) pair counts as a step, and the whole number above the log2 of such a count.
+__device__ __forceinline__ float i4_size(uint32_t pair) {
+  return fmaxf(__uint_as_float(pair << 16), fabsf(__uint_as_float(pair & 0xFFFF0000u)) * 9.5367432e-7f);
+}
+__device__ __forceinline__ float i4_log2(float size) { return (float)(max(__float_as_int(size) >> 23, 38) - 126); }
+
 // 4 consumer warps, two CTAs per SM, 32 keys of a warp in flight. Measured against (us, 256K-token sequence /
 // mixed batch with drafts, cold L2; here 78 / 655): 6 warps 78 / 1001 (its 128 registers spill), 8 warps in
 // one CTA 113 / 721, 12 warps 115 / 1014, 16 keys in flight 111 / 752, 64 keys 111 / 655.
@@ -108,6 +117,7 @@ constexpr int I4_WARPS = 4;
 constexpr int I4_CTAS = 2;
 constexpr int I4_KU = 2;  // 16-key groups
 constexpr int I4_THREADS = (I4_WARPS + 1) * 32;
+constexpr float I4_NO_OFF = -1e30f;  // the offset of a row that has seen no key: any key moves it, and none weighs 0
 
 // One work item as the producer hands it to the consumers.
 struct I4Item {
@@ -138,7 +148,7 @@ struct I4Smem {
   static constexpr int AREA_OFF = Q_OFF + SLOTS * Q_BYTES;
   static constexpr int AREAS = SOLO ? 0 : I4_WARPS / RG;  // one per warp of a row group
   static constexpr int ML_OFF = AREA_OFF + AREAS * ROWS * AREA_STRIDE * 4;
-  // m, l, sum p lo per (warp, row), then per row
+  // offset, l, sum p lo per (warp, row), then per row
   static constexpr int ROW_OFF = ML_OFF + (SOLO ? 0 : (3 * I4_WARPS * ROWS + 3 * ROWS) * 4);  // per row: token, output offset
   static constexpr int ITEM_OFF = ROW_OFF + 2 * ROWS * 4;
   static constexpr int MAX_NS = 32;
@@ -468,7 +478,7 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
   const int row0 = rg * 8 * NT;
   // key of S^T row g8 within a 16-key group (row g8 + 8: + 8), see the header comment
   const int pi0 = (g8 & 1) ? 4 + ((g8 >> 1) ^ 1) : g8 >> 1;
-  float* m_w = reinterpret_cast<float*>(smem + SM::ML_OFF);  // [KW][ROWS]
+  float* m_w = reinterpret_cast<float*>(smem + SM::ML_OFF);  // [KW][ROWS] offsets (-inf: no key seen)
   float* l_w = m_w + I4_WARPS * ROWS;
   float* b_w = l_w + I4_WARPS * ROWS;
   float* m_all = b_w + I4_WARPS * ROWS;
@@ -551,13 +561,13 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
     }
 
     float o[MT][NT][4];
-    float m[NT][2], l[NT][2], bs[NT][2];
-    float ws[NT][2];  // sum of the weights as V takes them (p step 2^-e_cur) since they last left O, see below
+    float off[NT][2], l[NT][2], bs[NT][2];
+    float ws[NT][2];  // sum of the weights as V takes them (p step) since they last left O, see below
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        m[nt][c] = -INFINITY;
+        off[nt][c] = I4_NO_OFF;
         l[nt][c] = 0.f;
         bs[nt][c] = 0.f;
         ws[nt][c] = 0.f;
@@ -566,9 +576,6 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
     for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
-    int e_cur = -120;        // V steps are used divided by 2^e_cur
-    float fe = pow2i(120);   // 2^-e_cur
-    float sv_lim = -1.f;     // a step above this moves e_cur
     uint32_t n_done = 0;     // blocks this warp has added to O
     const int lo_min = I.lo_min, lo_max = I.lo_max, hi_min = I.hi_min, hi_max = I.hi_max;
 
@@ -631,13 +638,11 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
             }
         }
         // ---- scores in the log2 domain, masks
-        bool move = false;
 #pragma unroll
         for (int u = 0; u < KU; ++u) {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const float ksf = __uint_as_float(kp[u][k] << 16), klf = __uint_as_float(kp[u][k] & 0xFFFF0000u);
-            move = move || __uint_as_float(vp[u][k] << 16) > sv_lim;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -669,6 +674,13 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
                 }
             }
         }
+        // Does a row's largest score go with the largest step of this lane's keys? (More than needed where they are
+        // two keys, or the step is one that the row does not see; which rows have to move is looked at below.)
+        float size = 0.f;
+#pragma unroll
+        for (int u = 0; u < KU; ++u) size = fmax3(size, i4_size(vp[u][0]), i4_size(vp[u][1]));
+        const float room = 15.f - i4_log2(size);
+        bool move = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -676,61 +688,43 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
             float mx = fmaxf(acc[0][nt][c], acc[0][nt][2 + c]);
 #pragma unroll
             for (int u = 1; u < KU; ++u) mx = fmax3(mx, acc[u][nt][c], acc[u][nt][2 + c]);
-            if constexpr (!MOD) mx *= c1[nt][c];
-            move = move || mx > m[nt][c] + 8.f;
+            move = move || (MOD ? mx - off[nt][c] : fmaf(mx, c1[nt][c], -off[nt][c])) > room;
           }
         if (__any_sync(0xffffffffu, move)) {
-          float smax = 0.f;
-#pragma unroll
-          for (int u = 0; u < KU; ++u)
-            smax = fmax3(smax, __uint_as_float(vp[u][0] << 16), __uint_as_float(vp[u][1] << 16));
-#pragma unroll
-          for (int x = 4; x < 32; x <<= 1) smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, x));
-          float osc = 1.f;
-          if (smax > sv_lim) {  // the same in every lane
-            int e = (int)((__float_as_uint(smax) >> 23) & 255u) - 127 - 6;  // steps at most 2^7
-            e = e < -120 ? -120 : e;
-            if (e > e_cur) {
-              osc = e - e_cur > 126 ? 0.f : pow2i(e_cur - e);
-              e_cur = e;
-              fe = pow2i(-e_cur);
-            }
-            sv_lim = e_cur >= 120 ? 3.4e38f : pow2i(e_cur + 7);
-          }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              float mx = fmaxf(acc[0][nt][c], acc[0][nt][2 + c]);
+              float mx = -INFINITY;  // the largest log2 (p step) but for the offset
 #pragma unroll
-              for (int u = 1; u < KU; ++u) mx = fmax3(mx, acc[u][nt][c], acc[u][nt][2 + c]);
+              for (int u = 0; u < KU; ++u)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const float lq = i4_log2(i4_size(vp[u][k]));
+                  mx = fmaxf(mx, MOD ? acc[u][nt][2 * k + c] + lq : fmaf(acc[u][nt][2 * k + c], c1[nt][c], lq));
+                }
 #pragma unroll
               for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-              if constexpr (!MOD) mx *= c1[nt][c];
-              const float mn = fmaxf(m[nt][c], mx);
-              const float al = mn == -INFINITY ? 1.f : ex2_approx(m[nt][c] - mn);
-              m[nt][c] = mn;
-              l[nt][c] *= al;
-              bs[nt][c] *= al;
-              const float f = al * osc;
-              ws[nt][c] *= f;
+              if (mx - off[nt][c] > 15.f) {  // the same in the row's lanes
+                const float to = ceilf(mx) - 7.f;
+                const float f = ex2_approx(off[nt][c] - to);
+                off[nt][c] = to;
+                l[nt][c] *= f;
+                bs[nt][c] *= f;
+                ws[nt][c] *= f;
 #pragma unroll
-              for (int i = 0; i < MT; ++i) {
-                o[i][nt][c] *= f;
-                o[i][nt][2 + c] *= f;
+                for (int i = 0; i < MT; ++i) {
+                  o[i][nt][c] *= f;
+                  o[i][nt][2 + c] *= f;
+                }
               }
             }
         }
         // ---- softmax weights, O^T += V^T P^T
-        float moff[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) moff[nt][c] = m[nt][c] == -INFINITY ? 0.f : m[nt][c];
 #pragma unroll
         for (int u = 0; u < KU; ++u) {
           uint32_t pb[NT][2];
-          const float vsf[2] = {__uint_as_float(vp[u][0] << 16) * fe, __uint_as_float(vp[u][1] << 16) * fe};
+          const float vsf[2] = {__uint_as_float(vp[u][0] << 16), __uint_as_float(vp[u][1] << 16)};
           const float vlf[2] = {__uint_as_float(vp[u][0] & 0xFFFF0000u), __uint_as_float(vp[u][1] & 0xFFFF0000u)};
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
@@ -742,8 +736,8 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
               float e[2];
 #pragma unroll
               for (int c = 0; c < 2; ++c)
-                e[c] = ex2_approx(MOD ? acc[u][nt][2 * k + c] - moff[nt][c]
-                                      : fmaf(acc[u][nt][2 * k + c], c1[nt][c], -moff[nt][c]));
+                e[c] = ex2_approx(MOD ? acc[u][nt][2 * k + c] - off[nt][c]
+                                      : fmaf(acc[u][nt][2 * k + c], c1[nt][c], -off[nt][c]));
               const uint64_t e2 = f2_pack(e[0], e[1]);
               l2 = f2_add(l2, e2);
               b2 = f2_fma(e2, f2_pack(vlf[k], vlf[k]), b2);
@@ -807,7 +801,7 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) d += __shfl_xor_sync(0xffffffffu, d, x);
             const float S = 7.5f * d;
-            bs[nt][c] = fmaf(0.125f * S, pow2i(e_cur), bs[nt][c]);  // the 8 lanes of a row are summed at the end
+            bs[nt][c] = fmaf(0.125f, S, bs[nt][c]);  // the 8 lanes of a row are summed at the end
             const float se = S * 5.9604645e-8f, so = S * 9.5367432e-7f;  // 2^-24, 2^-20
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
@@ -839,12 +833,12 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
         for (int c = 0; c < 2; ++c) {
           const int r = row0 + nt * 8 + 2 * t4 + c;
           const float inv = l[nt][c] == 0.f ? 0.f : 1.f / l[nt][c];  // (a row that sees nothing: 0)
-          const float fo = pow2i(e_cur), b0 = bs[nt][c];
+          const float b0 = bs[nt][c];
           uint32_t w[MT];
 #pragma unroll
           for (int i = 0; i < MT; ++i)
-            w[i] = pack_bf16x2(fmaf(o[i][nt][c] * fo, 16777216.f, b0) * inv,
-                               fmaf(o[i][nt][2 + c] * fo, 1048576.f, b0) * inv);
+            w[i] = pack_bf16x2(fmaf(o[i][nt][c], 16777216.f, b0) * inv,
+                               fmaf(o[i][nt][2 + c], 1048576.f, b0) * inv);
           if (r < p.R) {
             uint4* dst = reinterpret_cast<uint4*>(out + row_out[r] + g8 * (D / 8));
 #pragma unroll
@@ -863,7 +857,7 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int r = row0 + nt * 8 + 2 * t4 + c;
-          m_w[kw * ROWS + r] = m[nt][c];
+          m_w[kw * ROWS + r] = off[nt][c] == I4_NO_OFF ? -INFINITY : off[nt][c];
           l_w[kw * ROWS + r] = l[nt][c];
           b_w[kw * ROWS + r] = bs[nt][c];
         }
@@ -895,7 +889,7 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
           float M = -INFINITY;
 #pragma unroll
           for (int w = 0; w < KW; ++w) M = fmaxf(M, m_w[w * ROWS + r]);
-          f[nt][c] = M == -INFINITY ? 0.f : ex2_approx(m[nt][c] - M) * pow2i(e_cur);
+          f[nt][c] = M == -INFINITY ? 0.f : ex2_approx(off[nt][c] - M);
         }
       // O^T accumulators: dims 2i hold 2^-24, dims 2i + 1 hold 2^-20 of the sum
       {
