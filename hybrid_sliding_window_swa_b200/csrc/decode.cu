@@ -142,6 +142,15 @@ __device__ __forceinline__ int64_t safe_len(const DecParams& p, int s) {
   return L;
 }
 
+// What a launch does to its scores: nothing, hswa_score_mod with a cap up to kSmallCap (or none), or with a larger
+// one. (One kernel for both kinds of caps would be slower for the small ones: 2.5% on 48 contexts of 512 to 32768 keys.)
+enum : int { PLAIN = 0, MODIFIED = 1, LARGE_CAP = 2 };
+
+template <int MODE>
+__device__ __forceinline__ float capped_score(float z, float in, float out) {
+  return MODE == LARGE_CAP ? capped_log2_any(z, in, out) : capped_log2(z, in, out);
+}
+
 // Extended launches: positions row t of sequence s may see, [lo, hi), within [0, L + n_qt) and (SWA)
 // within the window on both sides. hi <= lo: nothing.
 __device__ __forceinline__ void row_range(const DecParams& p, int s, int64_t L, int t, int& lo, int& hi) {
@@ -423,11 +432,12 @@ struct DecSmem {
 //    tokens are quantized with the layer's reciprocal scales as they are staged, the values the
 //    cache holds once they are committed.
 //
-// EXT: splits of p.split keys, per-row key ranges, capped scores and a distance bias (row_range; the
+// EXT (MODE not PLAIN): splits of p.split keys, per-row key ranges, capped scores and a distance bias (row_range; the
 // ranges replace the causal bound, the scores take cap tanh(s / cap) - slope |i - j|). Keys no row
 // sees are filled with zeros or masked, and a row that sees nothing gives zeros.
-template <int D, int MT, bool FP8, bool EXT>
+template <int D, int MT, bool FP8, int MODE>
 __global__ void __launch_bounds__(DEC_THREADS, 2) decode_kernel(DecParams p) {
+  constexpr bool EXT = MODE != PLAIN;
   using SM = DecSmem<D, MT, FP8>;
   constexpr int ROWS = SM::ROWS;
   constexpr int NS = SM::NS;
@@ -784,10 +794,18 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) decode_kernel(DecParams p) {
           float v[4];
           if constexpr (EXT) {
 #pragma unroll
+            for (int x = 0; x < 4; ++x) v[x] = sacc[mt][x >> 1][hf * 2 + (x & 1)] * sl2;
+            if (MODE == LARGE_CAP || p.softcap > 0.f) {
+#pragma unroll
+              for (int x = 0; x < 4; ++x) v[x] = capped_score<MODE>(v[x], p.cap_in, p.cap_log2);
+            } else {
+#pragma unroll
+              for (int x = 0; x < 4; ++x) v[x] *= 1.4426950408889634f;
+            }
+#pragma unroll
             for (int x = 0; x < 4; ++x) {
               const int key = col_base + (x >> 1) * 8 + (x & 1);
-              float z = sacc[mt][x >> 1][hf * 2 + (x & 1)] * sl2;
-              z = p.softcap > 0.f ? capped_log2(z, p.cap_in, p.cap_log2) : z * 1.4426950408889634f;
+              float z = v[x];
               if (p.slope) z = fmaf(-row_sl[mt][hf], (float)abs(row_pos[mt][hf] - key), z);
               if (need_mask && (key < row_lo[mt][hf] || key >= row_hi[mt][hf] || key >= (is_new ? L + p.n_qt : b)))
                 z = -INFINITY;
@@ -1245,16 +1263,17 @@ cudaError_t launch_merge_rows(const DecParams& p, int64_t max_splits, cudaStream
 #include "decode_tc.cuh"
 #include "decode_i4.cuh"
 
-template <int D, int MT, bool FP8, bool EXT>
+template <int D, int MT, bool FP8, int MODE>
 int launch_t(DecParams& p, int n_items_max, int sms, int64_t nsp_max, size_t merge_smem, cudaStream_t stream) {
+  constexpr bool EXT = MODE != PLAIN;
   using SM = DecSmem<D, MT, FP8>;
   plan_kernel<EXT><<<1, 1024, 0, stream>>>(p);
-  cudaFuncSetAttribute(decode_kernel<D, MT, FP8, EXT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::BYTES);
+  cudaFuncSetAttribute(decode_kernel<D, MT, FP8, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::BYTES);
   int per_sm = 2;
   int grid = sms * per_sm;
   if (grid > n_items_max) grid = n_items_max;
   if (grid < 1) grid = 1;
-  decode_kernel<D, MT, FP8, EXT><<<grid, DEC_THREADS, SM::BYTES, stream>>>(p);
+  decode_kernel<D, MT, FP8, MODE><<<grid, DEC_THREADS, SM::BYTES, stream>>>(p);
   cudaError_t e = cudaSuccess;
   if constexpr (EXT) {
     if (nsp_max > 1) e = launch_merge_rows<D>(p, nsp_max, stream);
@@ -1271,20 +1290,20 @@ int launch_t(DecParams& p, int n_items_max, int sms, int64_t nsp_max, size_t mer
   return HSWA_OK;
 }
 
-template <int D, int NT, int RG, bool MOD, bool SOLO>
+template <int D, int NT, int RG, int MODE, bool SOLO>
 int launch_i4(DecParams& p, int n_items_max, int sms, int device, int64_t nsp_max, cudaStream_t stream) {
   using SM = I4Smem<D, NT, RG, SOLO>;
-  HSWA_SET_SMEM((decode_i4_kernel<D, NT, RG, MOD, SOLO>), SM::BYTES, device);
+  HSWA_SET_SMEM((decode_i4_kernel<D, NT, RG, MODE, SOLO>), SM::BYTES, device);
   int grid = sms * I4_CTAS;
   if (grid > n_items_max) grid = n_items_max;
   if (grid < 1) grid = 1;
   p.small = p.n_seqs <= 32 ? 1 : 0;
   cudaError_t e = cudaSuccess;
   if (SOLO || p.small) {
-    decode_i4_kernel<D, NT, RG, MOD, SOLO><<<grid, I4_THREADS, SM::BYTES, stream>>>(p);
+    decode_i4_kernel<D, NT, RG, MODE, SOLO><<<grid, I4_THREADS, SM::BYTES, stream>>>(p);
   } else {
     plan_kernel<true><<<1, 1024, 0, stream>>>(p);
-    e = launch_dependent(decode_i4_kernel<D, NT, RG, MOD, SOLO>, grid, I4_THREADS, SM::BYTES, stream, p);
+    e = launch_dependent(decode_i4_kernel<D, NT, RG, MODE, SOLO>, grid, I4_THREADS, SM::BYTES, stream, p);
   }
   if (!SOLO && e == cudaSuccess && nsp_max > 1) e = launch_merge_rows<D>(p, nsp_max, stream);
   if (e == cudaSuccess) e = cudaGetLastError();
@@ -1410,28 +1429,25 @@ int launch_decode(const DecodeLaunch& Lc, cudaStream_t stream) {
   const int64_t nsp_max = max_splits(p.window, p.max_ctx_len, p.split);
   const size_t msm = decode_merge_smem_bytes(p.n_seqs, p.n_qt, p.Hq, p.Hkv, p.window, p.max_ctx_len);
   const int sms = pool->sms;
+  const int mode = !Lc.mod ? PLAIN : Lc.mod->softcap > kSmallCap ? LARGE_CAP : MODIFIED;
   if (pool->i4) {
     const bool solo = i4_teams(p.n_seqs, p.Hkv, p.R, p.window, p.max_ctx_len);  // a team of warps per item
-#define HSWA_I4_R(DD, MODD, SOLO_)                                                                  \
-  (p.R <= 8    ? launch_i4<DD, 1, 1, MODD, SOLO_>(p, nmax, sms, pool->device, nsp_max, stream)  \
-   : p.R <= 16 ? launch_i4<DD, 2, 1, MODD, SOLO_>(p, nmax, sms, pool->device, nsp_max, stream)  \
-               : launch_i4<DD, 2, 2, MODD, SOLO_>(p, nmax, sms, pool->device, nsp_max, stream))
-#define HSWA_I4(DD, MODD) (solo ? HSWA_I4_R(DD, MODD, true) : HSWA_I4_R(DD, MODD, false))
-    if (Lc.d == 128) return Lc.mod ? HSWA_I4(128, true) : HSWA_I4(128, false);
-    return Lc.mod ? HSWA_I4(64, true) : HSWA_I4(64, false);
+#define HSWA_I4_R(DD, MODE, SOLO_)                                                                  \
+  (p.R <= 8    ? launch_i4<DD, 1, 1, MODE, SOLO_>(p, nmax, sms, pool->device, nsp_max, stream)  \
+   : p.R <= 16 ? launch_i4<DD, 2, 1, MODE, SOLO_>(p, nmax, sms, pool->device, nsp_max, stream)  \
+               : launch_i4<DD, 2, 2, MODE, SOLO_>(p, nmax, sms, pool->device, nsp_max, stream))
+#define HSWA_I4(DD, MODE) (solo ? HSWA_I4_R(DD, MODE, true) : HSWA_I4_R(DD, MODE, false))
+#define HSWA_I4_D(MODE) (Lc.d == 128 ? HSWA_I4(128, MODE) : HSWA_I4(64, MODE))
+    return mode == PLAIN ? HSWA_I4_D(PLAIN) : mode == MODIFIED ? HSWA_I4_D(MODIFIED) : HSWA_I4_D(LARGE_CAP);
 #undef HSWA_I4_R
 #undef HSWA_I4
+#undef HSWA_I4_D
   }
-  if (Lc.mod) {
-#define HSWA_DEC(DD, MM, F8) launch_t<DD, MM, F8, true>(p, nmax, sms, nsp_max, msm, stream)
-    if (pool->fp8) {
-      if (Lc.d == 128) return p.R <= 16 ? HSWA_DEC(128, 1, true) : HSWA_DEC(128, 2, true);
-      return p.R <= 16 ? HSWA_DEC(64, 1, true) : HSWA_DEC(64, 2, true);
-    }
-    if (Lc.d == 128) return p.R <= 16 ? HSWA_DEC(128, 1, false) : HSWA_DEC(128, 2, false);
-    return p.R <= 16 ? HSWA_DEC(64, 1, false) : HSWA_DEC(64, 2, false);
-#undef HSWA_DEC
-  }
+#define HSWA_DEC(DD, MM, F8, MODE) launch_t<DD, MM, F8, MODE>(p, nmax, sms, nsp_max, msm, stream)
+#define HSWA_DEC_D(DD, F8, MODE) (p.R <= 16 ? HSWA_DEC(DD, 1, F8, MODE) : HSWA_DEC(DD, 2, F8, MODE))
+#define HSWA_DEC_F(F8, MODE) (Lc.d == 128 ? HSWA_DEC_D(128, F8, MODE) : HSWA_DEC_D(64, F8, MODE))
+  if (mode == MODIFIED) return pool->fp8 ? HSWA_DEC_F(true, MODIFIED) : HSWA_DEC_F(false, MODIFIED);
+  if (mode == LARGE_CAP) return pool->fp8 ? HSWA_DEC_F(true, LARGE_CAP) : HSWA_DEC_F(false, LARGE_CAP);
   // FP8 pools with head_dim 128 may run the tcgen05 kernel of decode_tc.cuh instead of the mma.sync
   // one: environment variable HSWA_DECODE_TC = 1 (full layers) or 2 (every layer), read once per
   // process; unset or 0 keeps decode_kernel, the faster of the two as measured.
@@ -1441,13 +1457,9 @@ int launch_decode(const DecodeLaunch& Lc, cudaStream_t stream) {
   }();
   if (pool->fp8 && Lc.d == 128 && (tc_mode >= 2 || (tc_mode == 1 && p.window <= 0)))
     return launch_tc(p, nmax, sms, msm, stream);
-#define HSWA_DEC(DD, MM, F8) launch_t<DD, MM, F8, false>(p, nmax, sms, nsp_max, msm, stream)
-  if (pool->fp8) {
-    if (Lc.d == 128) return p.R <= 16 ? HSWA_DEC(128, 1, true) : HSWA_DEC(128, 2, true);
-    return p.R <= 16 ? HSWA_DEC(64, 1, true) : HSWA_DEC(64, 2, true);
-  }
-  if (Lc.d == 128) return p.R <= 16 ? HSWA_DEC(128, 1, false) : HSWA_DEC(128, 2, false);
-  return p.R <= 16 ? HSWA_DEC(64, 1, false) : HSWA_DEC(64, 2, false);
+  return pool->fp8 ? HSWA_DEC_F(true, PLAIN) : HSWA_DEC_F(false, PLAIN);
+#undef HSWA_DEC_F
+#undef HSWA_DEC_D
 #undef HSWA_DEC
 }
 

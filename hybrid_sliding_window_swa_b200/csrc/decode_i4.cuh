@@ -162,8 +162,9 @@ struct I4Smem {
   using Ring = StageRing<NS>;
 };
 
-template <int D, int NT, int RG, bool MOD, bool SOLO>
+template <int D, int NT, int RG, int MODE, bool SOLO>
 __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParams p) {
+  constexpr bool MOD = MODE != PLAIN;
   using SM = I4Smem<D, NT, RG, SOLO>;
   constexpr int ROWS = SM::ROWS;
   constexpr int NS = SM::NS;
@@ -651,7 +652,7 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
                 if constexpr (MOD) {
                   const int key = kbase + k0 + 16 * u + pi0 + 8 * k;
                   z *= c1[nt][c];
-                  z = p.softcap > 0.f ? capped_log2(z, p.cap_in, p.cap_log2) : z * 1.4426950408889634f;
+                  z = MODE == LARGE_CAP || p.softcap > 0.f ? capped_score<MODE>(z, p.cap_in, p.cap_log2) : z * 1.4426950408889634f;
                   if (p.slope) z = fmaf(-slope[nt][c], (float)abs(r_pos[nt][c] - key), z);
                 }
                 acc[u][nt][2 * k + c] = z;

@@ -54,7 +54,7 @@ struct ScoreParams {
   float cap_in, cap_log2;  // 2 log2(e) scale / cap, cap log2 e
   float poly_max;          // raw scores up to this magnitude take the polynomial (0: none do)
   float poly[6];           // cap log2(e) tanh(x scale / cap) = x (poly[0] + poly[1] x^2 + ...)
-  float near_max;          // the same with three terms for |x| up to near_max = 0.35 cap / scale
+  float near_max;          // the same with three terms for |x| up to near_max = 0.35 (large caps: 0.125) cap / scale
   float near[3];
   const float* slope;      // [Hq] distance slopes, or null
   const int64_t* key_begin;  // [B][n_q], or null
@@ -73,18 +73,22 @@ inline void fill_score_params(const hswa_score_mod& m, double scale, ScoreParams
     sp->cap_log2 = (float)(log2e * m.softcap);
     // tanh(u) = u T(u^2) on |u| <= 1: interpolation at the 6 Chebyshev nodes of u^2 in [0, 1], off by at
     // most 5e-7. The powers of u's factor are folded into the coefficients, for caps whose folded
-    // coefficients and powers stay well inside the fp32 range.
+    // coefficients and powers stay well inside the fp32 range (c1 = scale / cap from 8e-8, the largest cap, to 100).
     const double T[6] = {0.9999993948006503,  -0.33328951370216614, 0.1328072064598301,
                          -0.05158598840417456, 0.01672085517953942, -0.0030582290375864097};
-    if (c1 >= 6e-4 && c1 <= 100.0) {
-      sp->poly_max = (float)(1.0 / c1);
-      // three terms on |u| <= 0.35, off by at most 1e-6
-      const double N[3] = {0.9999971183259196, -0.3329087359461866, 0.12394375936961438};
-      sp->near_max = (float)(0.35 / c1);
+    // Three terms on |u| <= 0.35, off by at most 1e-6. Both errors are the cap's share of a score's, so caps above
+    // 1 / 6e-4 of the scale (147 for d = 128) take neither: there the first three terms of the series serve on
+    // |u| <= 1/8, off by 2.1e-7 of the value, and only larger scores go through the exponential.
+    const double N[3] = {0.9999971183259196, -0.3329087359461866, 0.12394375936961438};
+    const double S[3] = {1.0, -1.0 / 3.0, 2.0 / 15.0};
+    const bool large = c1 < 6e-4;
+    if (c1 <= 100.0) {
+      sp->near_max = (float)((large ? 0.125 : 0.35) / c1);
+      if (!large) sp->poly_max = (float)(1.0 / c1);
       double f = log2e * m.softcap * c1;
       for (int i = 0; i < 6; ++i, f *= c1 * c1) {
-        sp->poly[i] = (float)(T[i] * f);
-        if (i < 3) sp->near[i] = (float)(N[i] * f);
+        if (!large) sp->poly[i] = (float)(T[i] * f);
+        if (i < 3) sp->near[i] = (float)((large ? S[i] : N[i]) * f);
       }
     }
   }
@@ -109,7 +113,7 @@ __device__ __forceinline__ float abs_max(const uint32_t (&v)[N]) {
 // The cap costs what tanh costs: through exponential and reciprocal it is two more MUFU operations per
 // score, on the unit that the softmax itself loads most. While every score of the warp stays within the
 // cap (|s| <= cap), the degree-11 polynomial on the FMA pipe replaces them: 7 packed multiply-adds per pair;
-// within 0.35 cap a degree-5 one does, 4 per pair.
+// within near_max a degree-5 one does, 4 per pair.
 // Bias: on a tile wholly before the warp's queries |c_q - k| = c_q - k, two packed operations per pair.
 // am: abs_max(v), used with a cap.
 template <int N>
@@ -148,9 +152,18 @@ __device__ __forceinline__ void modify_scores(uint32_t (&v)[N], const ScoreParam
         v[k + 1] = __float_as_uint(b);
       }
     } else {
+      // scores of every size: each takes the form that is exact for it (for tiny ones the exponential's is not)
+      const uint64_t n0 = f2_pack(sp.near[0], sp.near[0]), n1 = f2_pack(sp.near[1], sp.near[1]),
+                     n2 = f2_pack(sp.near[2], sp.near[2]);
 #pragma unroll
-      for (int k = 0; k < N; ++k)
-        v[k] = __float_as_uint(capped_log2(__uint_as_float(v[k]), sp.cap_in, sp.cap_log2));
+      for (int k = 0; k < N; k += 2) {
+        const float x0 = __uint_as_float(v[k]), x1 = __uint_as_float(v[k + 1]);
+        const uint64_t x = f2_pack(x0, x1), t = f2_mul(x, x);
+        float a, b;
+        f2_unpack(f2_mul(x, f2_fma(f2_fma(n2, t, n1), t, n0)), a, b);
+        v[k] = __float_as_uint(fabsf(x0) <= sp.near_max ? a : capped_log2(x0, sp.cap_in, sp.cap_log2));
+        v[k + 1] = __float_as_uint(fabsf(x1) <= sp.near_max ? b : capped_log2(x1, sp.cap_in, sp.cap_log2));
+      }
     }
     sl2 = 1.f;
   }
@@ -212,7 +225,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t trow, uint32_t s_col, uint
     reg_fence_into<32>(v);
     reg_fence_into<64>(v);
     reg_fence_into<96>(v);
-    // MOD: `near` = capped scores without a bias, all of the warp's within 0.35 cap. The cap is monotone,
+    // MOD: `near` = capped scores without a bias, all of the warp's within near_max. The cap is monotone,
     // so the row maximum is taken on raw scores and capped alone, and the three-term polynomial goes into
     // the exponential's argument: 3 packed operations per pair. (Masked scores, -inf, come out as -inf:
     // the polynomial's highest coefficient is positive.)
