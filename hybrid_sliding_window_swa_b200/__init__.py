@@ -309,16 +309,21 @@ class RopeDesc:
     n_axes: int = 1
     interleaved: bool = False
 
+    def __post_init__(self):  # a copy of its own: the C descriptor is built once
+        object.__setattr__(self, "inv_freq", tuple(map(float, self.inv_freq)))
+        if self.axis is not None:
+            object.__setattr__(self, "axis", tuple(map(int, self.axis)))
+
     def c(self):
         """Pointer to the C descriptor (built once)."""
         c = self.__dict__.get("_c")
         if c is None:
             n = len(self.inv_freq)
             axis = self.axis if self.axis is not None else [0] * n
-            if n > 64 or len(axis) != n or any(not 0 <= int(a) < 256 for a in axis):
+            if n > 64 or len(axis) != n or any(not 0 <= a < 256 for a in axis):
                 raise ValueError("one axis per frequency, at most 64 frequencies")
-            c = RopeDescC(2 * n, self.n_axes, int(self.interleaved), 0, (ctypes.c_double * 64)(*map(float, self.inv_freq)),
-                          (ctypes.c_uint8 * 64)(*map(int, axis)))
+            c = RopeDescC(2 * n, self.n_axes, int(self.interleaved), 0, (ctypes.c_double * 64)(*self.inv_freq),
+                          (ctypes.c_uint8 * 64)(*axis))
             object.__setattr__(self, "_c", ctypes.pointer(c))
             c = self.__dict__["_c"]
         return c
