@@ -314,6 +314,9 @@ class RopeDesc:
         if self.axis is not None:
             object.__setattr__(self, "axis", tuple(map(int, self.axis)))
 
+    def __getstate__(self):  # a copy builds its own C descriptor
+        return {k: v for k, v in self.__dict__.items() if k != "_c"}
+
     def c(self):
         """Pointer to the C descriptor (built once)."""
         c = self.__dict__.get("_c")

@@ -1,4 +1,7 @@
 """Without a GPU: the descriptor of rotary positions as a Python object."""
+import copy
+import pickle
+
 import torch
 
 import hybrid_sliding_window_swa_b200 as hs
@@ -17,3 +20,10 @@ def test_a_rope_descriptor_keeps_its_own_copy():
     assert rope == late and hash(rope) == hash(late) and before.inv_freq[0] == 1.0
     assert hs.RopeDesc(torch.tensor(inv, dtype=torch.float64)).inv_freq == tuple(inv)
     assert hs.RopeDesc(x for x in inv).c().contents.rot_dim == 16 and hs.RopeDesc(inv).axis is None
+
+
+def test_a_used_descriptor_can_be_copied_and_pickled():
+    rope = hs.RopeDesc([1.0 / (i + 1) for i in range(8)], [0] * 8, 1, True)
+    rope.c()
+    for other in (copy.deepcopy(rope), pickle.loads(pickle.dumps(rope))):
+        assert other == rope and other.c().contents.inv_freq[7] == 0.125 and other.c().contents.interleaved == 1
