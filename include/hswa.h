@@ -269,9 +269,10 @@ HSWA_API int hybrid_decode_fwd(hswa_pool* pool, int layer, const hswa_bf16* q, c
  * or of the new tokens (decode: ctx_len + n_q_per_seq). So packed documents pass the first position of
  * the query's document as key_begin; a prefix (or image) seen in both directions passes its end as
  * key_end; a padded row passes key_end <= key_begin. A query that sees no key gives zeros.
- * Keys a query does not see change nothing in its row, whatever they hold. Values must be finite between
- * the smallest and the largest position the queries of a sequence see; outside it they may hold anything,
- * and pages of such positions are not read. */
+ * Keys a query does not see add nothing to its row. Where other queries see them they can change its
+ * rounding: the order of its sums, and with a cap which of the formulas for tanh serves it, are chosen for
+ * several rows together. Values must be finite between the smallest and the largest position the queries of
+ * a sequence see; outside it they may hold anything, and pages of such positions are not read. */
 typedef struct hswa_score_mod {
   float softcap;             /* 0: none; else 1e-6 .. 1e6 */
   const float* dist_slope;   /* device float32[n_q_heads], finite; NULL: none */
