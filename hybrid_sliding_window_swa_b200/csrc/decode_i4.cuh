@@ -117,7 +117,7 @@ constexpr int I4_WARPS = 4;
 constexpr int I4_CTAS = 2;
 constexpr int I4_KU = 2;  // 16-key groups
 constexpr int I4_THREADS = (I4_WARPS + 1) * 32;
-constexpr float I4_NO_OFF = -1e30f;  // the offset of a row that has seen no key: any key moves it, and none weighs 0
+constexpr float I4_NO_OFF = -3e38f;  // the offset of a row that has seen no key: any key moves it
 
 // One work item as the producer hands it to the consumers.
 struct I4Item {
