@@ -31,13 +31,13 @@
 // counts as a step of 2^-20 of its size, and a step as at least 2^-89, which keeps sum p lo and l finite.
 //
 // What bounds it. 2 (d / 2 + 4) bytes per key and KV head. Up to 8 rows the reads do: 5.2 TB/s while the items
-// of a 256K-token sequence run (72 us the call; its 285 MB take 43 us). With 32 rows the instruction dispatch
-// does: integer 40%, MMA 40%, fp32 12% of the cycles (ncu), which add up; neither more warps nor more
+// of a 256K-token sequence run (70 us the call; its 285 MB take 43 us). With 32 rows the instruction dispatch
+// does: integer 40%, MMA 40%, fp32 14% of the cycles (ncu), which add up; neither more warps nor more
 // registers nor issuing the next block's S among the V products moved it.
 //
 // Structure: 4 consumer warps and a producer warp per CTA, two CTAs per SM, taking items from the work
 // list. A block is one 64-key page: (codes, pairs) of K and of V are contiguous, one bulk copy each
-// (cp.async for ring rows, whose runs may start anywhere), several blocks ahead, across items. The
+// (ring rows: the codes in one or two runs, the pairs row by row with cp.async), several blocks ahead, across items. The
 // producer also hands over the item's geometry and its Q rows. The warps take blocks in turn (for more
 // than 16 rows in pairs, half the rows each), 32 keys at a time so that enough independent MMAs are
 // in flight, and merge their softmax states at the end of the item.
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
   float* m_all = b_w + I4_WARPS * ROWS;
   float* l_all = m_all + ROWS;
   float* b_all = l_all + ROWS;
-  float* area = reinterpret_cast<float*>(smem + SM::AREA_OFF);  // [2][ROWS][AREA_STRIDE]
+  float* area = reinterpret_cast<float*>(smem + SM::AREA_OFF);  // [AREAS][ROWS][AREA_STRIDE]
   uint32_t ncons = 0;
   uint32_t n_issued = 0;  // as last read
   auto cons_sync = [&]() -> bool {
