@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 2) decode_kernel(DecParams p) {
     const int klo = (int)klo64, khi = (int)khi64;
     const int split = split_len<EXT>(p);
     const int a = klo + c * split;
-    const int b = (a + split < khi) ? a + split : khi;
+    const int b = khi - a > split ? a + split : khi;  // (a + split may pass 2^31)
     const int n_cached_blk = (b - a + KB - 1) / KB;
     int lo_all = 0, hi_all = 0x7fffffff;  // EXT: entries outside every row's range are not read
     if constexpr (EXT) {

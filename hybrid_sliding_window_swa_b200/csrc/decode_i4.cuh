@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(I4_THREADS, I4_CTAS) decode_i4_kernel(DecParam
       const int klo = (int)klo64, khi = (int)khi64;
       if (c < 0) c = nsp - 1;
       const int a = klo + c * p.split;
-      const int b = a + p.split < khi ? a + p.split : khi;
+      const int b = khi - a > p.split ? a + p.split : khi;  // (a + split may pass 2^31)
       const int n_cached = b > a ? (b - a + 63) / 64 : 0;
       const int n_blk = n_cached + (c == nsp - 1 ? 1 : 0);
       // visible range of each new token's rows, by lane
